@@ -3,7 +3,10 @@
  * (gfx950), dense and MoE-grouped, and the FP8 quantisation of activations
  * that produces its A operand.  The base calls take E4M3 operands with
  * 128x128 block scales; the _ex calls add E5M2 operands and per-token (1 x 128)
- * A scales, dg_grouped_gemm_fp8_segments serves decode-time MoE.
+ * A scales, dg_grouped_gemm_fp8_segments serves decode-time MoE.  The dg_moe_*,
+ * dg_swiglu_* and dg_grouped_wgrad_fp8 calls are what a mixture-of-experts layer
+ * needs around its products: tokens sorted by expert and back, the gated
+ * activation with an 8-bit checkpoint, and the backward passes.
  *
  * The operation (DeepGEMM FP8-for-MoE page, 2kiu.com/news/5461879,
  * section 2.1 "block-wise scaling"; FP32 accumulation, section 3.3):
@@ -318,6 +321,150 @@ typedef enum {
 int dg_quantize_fp8_blockscaled(const void* X, int in_dtype, void* Q, float* S,
                                 int64_t M, int64_t K, int block_rows,
                                 hipStream_t stream);
+
+/*
+ * The mixture-of-experts operators around the products: tokens sorted by expert
+ * and back, the gated activation between the two products of an expert, and
+ * the backward passes.  The shared conventions above apply (caller-owned device
+ * memory, asynchronous on `stream`, host-side argument checks before any HIP
+ * call, results bitwise repeatable, capturable into a HIP graph); none of
+ * these calls allocates.  Sums, dot products and exponentials are held in FP32
+ * or more; each output is rounded once.  "16-byte aligned" below covers every
+ * matrix; float32 and int32 arrays are 4-byte aligned (64-bit ids 8-byte).
+ * Sizes above 2^31 - 1 -> DG_ERR_INVALID_ARG, widths (H, I, N, K) above 2^22
+ * and more than 2^30 slots (T top_k) -> DG_ERR_UNSUPPORTED.
+ */
+typedef enum {
+  DG_IDX_I32 = 0,   /* expert ids are int32 */
+  DG_IDX_I64 = 1    /* expert ids are int64 */
+} dg_idx_dtype;
+
+typedef enum {
+  DG_SCALE_AMAX = 0,  /* s = fp32(amax / 448), as dg_quantize_fp8_blockscaled */
+  DG_SCALE_POW2 = 1   /* s = 2^ceil(log2(amax / 448)), at least 2^-126: decoded
+                         values are exact bfloat16 values */
+} dg_scale_mode;
+
+/*
+ * Tokens sorted by expert.  Slot s = t * top_k + j is token t's j-th choice and
+ * names expert ids[s]; a slot whose id lies outside [0, num_groups) is dropped.
+ * Expert e's slots, in slot order, take rows [o_e, o_e + count_e) of a sorted
+ * matrix of M_total rows whose segments are padded to `align` rows:
+ *
+ *   ids           : [T][top_k] ids_dtype
+ *   align         : 128 (segments of dg_grouped_gemm_fp8 and its forms) or 1
+ *                   (packed segments of dg_grouped_gemm_fp8_segments)
+ *   M_total       : a multiple of align, at least dg_moe_rows(): the most rows
+ *                   that any ids can need, so that no call has to wait for a
+ *                   count from the device
+ *   group_offsets : int32 [num_groups + 1]; o_G = M_total: the last segment
+ *                   takes the rows that are left, as padding
+ *   group_counts  : int32 [num_groups], real rows
+ *   row_slot      : int32 [M_total], the slot of a row, -1 for padding
+ *   slot_row      : int32 [T][top_k], the row of a slot, -1 when dropped
+ *   workspace     : dg_moe_sort_workspace() bytes (null if that is 0), in use
+ *                   until the work on `stream` is done
+ *
+ * T == 0 is not empty work: the offsets and counts are written.  num_groups
+ * above 1024 -> DG_ERR_UNSUPPORTED.
+ */
+int dg_moe_sort(const void* ids, int ids_dtype, int64_t T, int top_k, int num_groups, int align,
+                int64_t M_total, int32_t* group_offsets, int32_t* group_counts, int32_t* row_slot,
+                int32_t* slot_row, void* workspace, hipStream_t stream);
+
+/* Host only: the least M_total of dg_moe_sort, floor((T top_k + (align - 1)
+ * min(num_groups, T top_k)) / align) align; its workspace in bytes.  A
+ * negative dg_status for arguments dg_moe_sort refuses. */
+int64_t dg_moe_rows(int64_t T, int top_k, int num_groups, int align);
+int64_t dg_moe_sort_workspace(int64_t T, int top_k, int num_groups);
+
+/*
+ * Rows gathered into the sorted order, Y[r] = X[row_slot[r] / top_k]; rows of
+ * padding are zeros.  X [T][H] and Y [M_total][H] are of `dtype` (dg_in_dtype),
+ * any H.  slot_row and row_slot are dg_moe_sort's; entries of slot_row outside
+ * [0, M_total) are skipped.  Its gradient is dg_moe_combine without weights.
+ */
+int dg_moe_permute(const void* X, int dtype, void* Y, const int32_t* slot_row, const int32_t* row_slot,
+                   int64_t T, int top_k, int64_t M_total, int64_t H, hipStream_t stream);
+
+/*
+ * The same, quantised on the way: E4M3FN codes Q [M_total][H] and scales
+ * S float32 [M_total][ceil(H/128)], one per row and 128 columns (the last block
+ * may be partial): the A operand of the grouped products with sa_rows = 1.
+ * Codes are the E4M3FN values nearest to x / s (ties to even, capped at 448)
+ * and s = 1 for an all-zero block and in padding rows.  H must be a multiple of
+ * 16 (DG_ERR_UNSUPPORTED).  Non-finite inputs give unspecified codes.
+ */
+int dg_moe_permute_fp8(const void* X, int in_dtype, void* Q, float* S, int scale_mode,
+                       const int32_t* slot_row, const int32_t* row_slot, int64_t T, int top_k,
+                       int64_t M_total, int64_t H, hipStream_t stream);
+
+/*
+ * Back to token order: out[t] = sum over j of weights[t][j] Y[slot_row[t][j]],
+ * in the order of j; dropped slots (slot_row outside [0, M_total)) add nothing
+ * and their weights are not used, a token without slots gives zeros, and rows
+ * of padding are never read.  weights float32 [T][top_k], or null: all ones.
+ * Y [M_total][H] and out [T][H] are of `dtype`, any H.
+ */
+int dg_moe_combine(const void* Y, int dtype, const float* weights, const int32_t* slot_row, void* out,
+                   int64_t T, int top_k, int64_t M_total, int64_t H, hipStream_t stream);
+
+/*
+ * Its gradient: dY[slot_row[t][j]] = weights[t][j] dOut[t], zeros in rows of
+ * padding; dweights[t][j] = <dOut[t], Y[slot_row[t][j]]>, 0 for a dropped slot.
+ * dOut [T][H], Y and dY [M_total][H] of `dtype`, dweights float32 [T][top_k].
+ */
+int dg_moe_combine_bwd(const void* dOut, const void* Y, int dtype, const float* weights,
+                       const int32_t* slot_row, const int32_t* row_slot, void* dY, float* dweights,
+                       int64_t T, int top_k, int64_t M_total, int64_t H, hipStream_t stream);
+
+/*
+ * The gated activation between the two products, its input kept in 8 bits for
+ * the backward pass.  H [M][2 I] (dg_in_dtype) holds g in columns [0, I) and u
+ * in [I, 2 I); a = u g / (1 + exp(-g)), computed from them without rounding in
+ * between.  Ib = ceil(I/128), power-of-two scales (DG_SCALE_POW2):
+ *
+ *   A  : E4M3FN [M][I], sA float32 [M][Ib]: codes and scales of a (the A
+ *        operand of the second product, sa_rows = 1)
+ *   Hq : E4M3FN [M][2 I], sH float32 [M][2][Ib]: codes and scales of g and of
+ *        u; both null: no checkpoint is kept
+ *
+ * I must be a multiple of 16 (DG_ERR_UNSUPPORTED).  Non-finite inputs give
+ * unspecified codes.
+ */
+int dg_swiglu_fp8(const void* H, int in_dtype, void* A, float* sA, void* Hq, float* sH, int64_t M,
+                  int64_t I, hipStream_t stream);
+
+/*
+ * Its gradient from the checkpoint: with g, u decoded from Hq, sH and p =
+ * 1 / (1 + exp(-g)), dH[:, :I] = dA u p (1 + g (1 - p)) and dH[:, I:] = dA g p.
+ * dA [M][I] and dH [M][2 I] are of `dtype`.  I a multiple of 16.
+ */
+int dg_swiglu_fp8_bwd(const void* dA, int dtype, const void* Hq, const float* sH, void* dH, int64_t M,
+                      int64_t I, hipStream_t stream);
+
+/*
+ * Weight gradient of the grouped product from 8-bit activations:
+ *
+ *   dW_e[n][k] = sum over expert e's rows r of dY[r][n] s[r][k/128] dec(X[r][k])
+ *
+ *   dY : bfloat16 [M_total][N]; X : E4M3FN [M_total][K]; sX : float32
+ *        [M_total][ceil(K/128)]
+ *   group_offsets, group_counts : expert e's rows are [o_e, o_e + count_e), or
+ *        whole segments when group_counts is null; other rows are not used,
+ *        whatever they hold.  Offsets need no alignment and are clamped into
+ *        [0, M_total], counts into their segment.
+ *   dW : [num_groups][N][K] float32 or bfloat16 (out_dtype); accumulate = 1
+ *        adds to what it holds, 0 overwrites it (zeros for an expert without
+ *        rows)
+ *
+ * s dec(X) enters the products rounded to bfloat16, which changes nothing when
+ * the scales are powers of two.  N a multiple of 8 and K of 16
+ * (DG_ERR_UNSUPPORTED).
+ */
+int dg_grouped_wgrad_fp8(const void* dY, const void* X, const float* sX, const int32_t* group_offsets,
+                         const int32_t* group_counts, int num_groups, int64_t M_total, int64_t N,
+                         int64_t K, void* dW, int out_dtype, int accumulate, hipStream_t stream);
 
 /* Static, NUL-terminated description of a dg_status value. */
 const char* dg_status_string(int status);

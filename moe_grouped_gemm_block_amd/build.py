@@ -2,8 +2,8 @@
 
     python -m moe_grouped_gemm_block_amd.build
 
-Each source under csrc/ (the host side plus one translation unit per pair of
-operand formats, see csrc/kernels.hpp) is compiled to an object in parallel,
+Each source under csrc/ (the host side, one translation unit per pair of operand
+formats, see csrc/kernels.hpp, and the operators around the products) is compiled to an object in parallel,
 then the objects are linked into libdg.so.  Packed FP32 instructions are
 disabled for the device code (the host pass warns that it does not know the
 feature; that warning is harmless).
@@ -24,7 +24,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libdg.so")
 LIB_STAGES1 = os.path.join(PKG, "libdg_stages1.so")
 SOURCES = ["dg_api.hip", "kernels_e4m3.hip", "kernels_e4m3_e5m2.hip", "kernels_e5m2_e4m3.hip",
-           "kernels_e5m2.hip"]
+           "kernels_e5m2.hip", "moe_api.hip"]
 ARCH = os.environ.get("DG_OFFLOAD_ARCH", "gfx950")
 HARMLESS = "packed-fp32-ops' is not a recognized feature"
 

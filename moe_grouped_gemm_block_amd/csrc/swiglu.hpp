@@ -1,0 +1,221 @@
+// The gated activation between an expert's two products, with its input kept
+// in 8 bits for the backward pass, gfx950.
+//
+//   h = [g | u] (one row of the first product), a = u g / (1 + e^-g)
+//   forward   A, sA = codes and scales of a      (the second product's operand)
+//             Hq, sH = codes and scales of g and of u   (the checkpoint)
+//   backward  from g, u as the checkpoint holds them, p = 1 / (1 + e^-g):
+//             dg = dA u p (1 + g (1 - p)),  du = dA g p
+//
+// Scales are powers of two, one per row and 128 columns of a, g and u each:
+// moving a float by a power of two does not round, so the only rounding of the
+// checkpoint is the one to E4M3's four significant bits, and decoded values are
+// exact BF16 values (which the weight gradient's matrix product relies on).
+//
+// Both passes are bound by memory: forward 4 bytes in and 3 out per element
+// pair, backward 4 in and 4 out.  An 8-lane group takes one block of 128
+// columns, 16 values of g, u and a per lane in registers; the block maxima are
+// reduced by lane permutations, nothing goes through LDS.
+//
+// The codes of a are those of the real number u g / (1 + e^-g) rounded once, not
+// of its FP32 approximation: a fast FP32 value within 2^-21 of it is encoded at
+// both ends of a bracket of +-2^-20, and where the two codes differ (about one
+// value in 2^16) or FP32's range gets in the way, it is computed again in
+// double.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "common.hpp"
+#include "moe.hpp"
+#include "quant.hpp"
+
+namespace dg {
+
+struct SwigluArgs {
+  const void* H;         // [M][2 I]
+  uint8_t* A;            // [M][I] codes
+  float* sA;             // [M][Ib]
+  uint8_t* Hq;           // [M][2 I] codes, or null: no checkpoint
+  float* sH;             // [M][2][Ib]
+  int M, I, Ib;
+};
+
+// e^-g within 2^-22 of it: the exponent's product with log2(e) keeps its
+// rounding error as a second term (FP32's alone would cost |g| 2^-24).
+// g >= -80.
+__device__ __forceinline__ float exp_neg(float g) {
+  constexpr float L = 1.44269504088896341f, L_LO = 1.92596299e-8f;   // log2(e) = L + L_LO
+  const float hi = -g * L;
+  const float lo = __builtin_fmaf(-g, L, -hi) - g * L_LO;
+  const float e = __builtin_amdgcn_exp2f(hi);
+  return __builtin_fmaf(e, lo * 0.693147180559945f, e);
+}
+
+__device__ __forceinline__ double silu_mul_f64(float g, float u) {
+  const double gd = g;
+  return double(u) * (gd / (1.0 + exp(-gd)));
+}
+
+// u g / (1 + e^-g) within 2^-21 (results below FP32's normal range aside)
+__device__ __forceinline__ float silu_mul(float g, float u) {
+  if (g < -80.f) return float(silu_mul_f64(g, u));            // e^-g would leave FP32's range
+  return u * (g * __builtin_amdgcn_rcpf(1.f + exp_neg(g)));
+}
+
+// E4M3 code of v (|v| <= 448 or a little above it), rounded once.
+__device__ __forceinline__ uint32_t e4m3_of_f64(double v) {
+  const double m = fmin(__builtin_fabs(v), 448.0);
+  const int e = max(__builtin_amdgcn_frexp_exp(m), -5);       // v = [0.5, 1) 2^e; grid step 2^(e - 4)
+  const float q = float(__builtin_ldexp(__builtin_rint(__builtin_ldexp(m, 4 - e)), e - 4));
+  return hw_codes4(float(__builtin_copysign(double(q), v)), 0.f, 0.f, 0.f) & 0xFFu;
+}
+
+template <bool IN_BF16, bool CHECKPOINT>
+__device__ __forceinline__ void swiglu_body(const SwigluArgs& p) {
+  const int lane = threadIdx.x & 63;
+  const long long blk = (long long)blockIdx.x * 32 + (threadIdx.x >> 3);
+  const int m = int(blk / p.Ib);
+  const int ib = int(blk - (long long)m * p.Ib);
+  const int col = ib * 128 + 16 * (lane & 7);
+  const bool in = m < p.M && col < p.I;
+  Q1Buf<IN_BF16> bg, bu;
+  const size_t e0 = in ? size_t(m) * 2 * p.I + col : 0;
+  load_q16(bg, p.H, e0, in);
+  load_q16(bu, p.H, e0 + (in ? p.I : 0), in);
+  float a[16], ga = 0.f, ua = 0.f, aa = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float g = q1_value(bg, i), u = q1_value(bu, i);
+    a[i] = silu_mul(g, u);
+    ga = fmaxf(ga, __builtin_fabsf(g));
+    ua = fmaxf(ua, __builtin_fabsf(u));
+    aa = fmaxf(aa, __builtin_fabsf(a[i]));
+  }
+  aa = group8_max(aa);
+  if constexpr (CHECKPOINT) {
+    ga = group8_max(ga);
+    ua = group8_max(ua);
+    float sg, su;
+    const Codes16 cg = encode16<true>([&](int i) { return q1_value(bg, i); }, ga, sg);
+    const Codes16 cu = encode16<true>([&](int i) { return q1_value(bu, i); }, ua, su);
+    if (in) {
+      store16<true>(p.Hq + e0, u32x4_nt{cg.w[0], cg.w[1], cg.w[2], cg.w[3]});
+      store16<true>(p.Hq + e0 + p.I, u32x4_nt{cu.w[0], cu.w[1], cu.w[2], cu.w[3]});
+    }
+    if (m < p.M && (lane & 7) == 0) {
+      p.sH[(size_t(m) * 2) * p.Ib + ib] = sg;
+      p.sH[(size_t(m) * 2 + 1) * p.Ib + ib] = su;
+    }
+  }
+
+  // the scale of a's block, from the maximum in reals
+  int e = 0;
+  bool some = aa > 0.f, all64 = false;
+  if (some) {
+    e = pow2_exponent(aa * (1.f - 0x1p-20f));
+    all64 = e < -90;                      // values near FP32's lower end: no bracket is trusted
+    if (all64 || e != pow2_exponent(aa * (1.f + 0x1p-20f))) {
+      double md = 0.0;
+#pragma unroll 1
+      for (int i = 0; i < 16; ++i) {
+        float g = 0.f, u = 0.f;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {    // registers are not indexed by a variable
+          g = i == k ? q1_value(bg, k) : g;
+          u = i == k ? q1_value(bu, k) : u;
+        }
+        md = fmax(md, __builtin_fabs(silu_mul_f64(g, u)));
+      }
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) md = fmax(md, __shfl_xor(md, o, 64));
+      const double mant = __builtin_amdgcn_frexp_mant(md);
+      e = max(__builtin_amdgcn_frexp_exp(md) - (mant > 0.875 ? 8 : 9), -126);
+      some = md > 0.0;
+    }
+  }
+  const float s = some ? pow2f(e) : 1.f, r = some ? pow2f(-e) : 1.f;
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float r_lo = r * (1.f - 0x1p-20f), r_hi = r * (1.f + 0x1p-20f);
+    w[j] = hw_codes4(a[4 * j] * r_lo, a[4 * j + 1] * r_lo, a[4 * j + 2] * r_lo, a[4 * j + 3] * r_lo);
+    const uint32_t hi = hw_codes4(a[4 * j] * r_hi, a[4 * j + 1] * r_hi, a[4 * j + 2] * r_hi, a[4 * j + 3] * r_hi);
+    if (w[j] != hi || all64) {
+      uint32_t c = 0;
+#pragma unroll 1
+      for (int i = 0; i < 4; ++i) {
+        float g = 0.f, u = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          g = i == k ? q1_value(bg, 4 * j + k) : g;
+          u = i == k ? q1_value(bu, 4 * j + k) : u;
+        }
+        c |= e4m3_of_f64(silu_mul_f64(g, u) * double(r)) << (8 * i);
+      }
+      w[j] = c;
+    }
+  }
+  if (in) store16<true>(p.A + size_t(m) * p.I + col, u32x4_nt{w[0], w[1], w[2], w[3]});
+  if (m < p.M && (lane & 7) == 0) p.sA[size_t(m) * p.Ib + ib] = s;
+}
+
+struct SwigluBwdArgs {
+  const void* dA;        // [M][I]
+  const uint8_t* Hq;     // [M][2 I] codes
+  const float* sH;       // [M][2][Ib]
+  void* dH;              // [M][2 I]
+  int M, I, Ib;
+};
+
+typedef float v2f __attribute__((ext_vector_type(2)));
+
+// Four E4M3 codes -> their values times s.
+__device__ __forceinline__ void decode4(uint32_t w, float s, float* v) {
+  const v2f lo = __builtin_amdgcn_cvt_pk_f32_fp8(int(w), false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(int(w), true);
+  v[0] = lo.x * s;
+  v[1] = lo.y * s;
+  v[2] = hi.x * s;
+  v[3] = hi.y * s;
+}
+
+// A thread takes 8 columns: 8 codes of g and of u and 8 values of dA in, 8
+// values of dg and of du out.  FP32 throughout, one rounding to the output type.
+template <bool BF16>
+__device__ __forceinline__ void swiglu_bwd_body(const SwigluBwdArgs& p) {
+  const int per = p.I / 8;
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  const int m = int(i / per);
+  if (m >= p.M) return;
+  const int col = int(i - (long long)m * per) * 8;
+  const size_t h0 = size_t(m) * 2 * p.I + col;
+  const uint2 wg = *reinterpret_cast<const uint2*>(p.Hq + h0);
+  const uint2 wu = *reinterpret_cast<const uint2*>(p.Hq + h0 + p.I);
+  const float sg = p.sH[(size_t(m) * 2) * p.Ib + col / 128], su = p.sH[(size_t(m) * 2 + 1) * p.Ib + col / 128];
+  float g[8], u[8], d[8], dg_[8], du[8];
+  decode4(wg.x, sg, g);
+  decode4(wg.y, sg, g + 4);
+  decode4(wu.x, su, u);
+  decode4(wu.y, su, u + 4);
+  constexpr int V = BF16 ? 8 : 4;
+#pragma unroll
+  for (int v = 0; v < 8; v += V) load_values<BF16, V>(p.dA, size_t(m) * p.I + col + v, d + v);
+#pragma unroll
+  for (int v = 0; v < 8; ++v) {
+    // p = 1 / (1 + e) and 1 - p = e p, which keeps its relative precision where
+    // p is near 1; below -80 p and both factors are taken as at -80 (2^-115)
+    const float e = exp_neg(fmaxf(g[v], -80.f));
+    const float pr = __builtin_amdgcn_rcpf(1.f + e);
+    const float x = g[v] * pr;
+    du[v] = d[v] * x;
+    dg_[v] = d[v] * u[v] * __builtin_fmaf(x, e * pr, pr);
+  }
+#pragma unroll
+  for (int v = 0; v < 8; v += V) {
+    store_values<BF16, V>(p.dH, h0 + v, dg_ + v);
+    store_values<BF16, V>(p.dH, h0 + p.I + v, du + v);
+  }
+}
+
+}  // namespace dg

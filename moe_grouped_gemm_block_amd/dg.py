@@ -11,8 +11,10 @@ fallback implementation.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
+from typing import NamedTuple
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("DG_LIBRARY", os.path.join(_PKG, "libdg.so"))
@@ -23,6 +25,10 @@ DG_IN_F32 = 0
 DG_IN_BF16 = 1
 DG_FP8_E4M3 = 0
 DG_FP8_E5M2 = 1
+DG_IDX_I32 = 0
+DG_IDX_I64 = 1
+DG_SCALE_AMAX = 0
+DG_SCALE_POW2 = 1
 DG_OK = 0
 DG_ERR_INVALID_ARG = -1
 DG_ERR_UNSUPPORTED = -2
@@ -30,7 +36,9 @@ DG_ERR_LAUNCH = -3
 
 EXPORTED = ("dg_gemm_fp8_blockscaled", "dg_grouped_gemm_fp8", "dg_gemm_fp8_ex", "dg_gemm_fp8_ex_noalloc",
             "dg_grouped_gemm_fp8_ex", "dg_grouped_gemm_fp8_ex_counts", "dg_grouped_gemm_fp8_segments",
-            "dg_quantize_fp8_blockscaled", "dg_status_string")
+            "dg_quantize_fp8_blockscaled", "dg_moe_sort", "dg_moe_rows", "dg_moe_sort_workspace",
+            "dg_moe_permute", "dg_moe_permute_fp8", "dg_moe_combine", "dg_moe_combine_bwd", "dg_swiglu_fp8",
+            "dg_swiglu_fp8_bwd", "dg_grouped_wgrad_fp8", "dg_status_string")
 
 _lib = None
 
@@ -74,6 +82,26 @@ def lib() -> ctypes.CDLL:
         L.dg_grouped_gemm_fp8_segments.restype = ci
         L.dg_quantize_fp8_blockscaled.argtypes = [vp, ci, vp, vp, i64, i64, ci, vp]
         L.dg_quantize_fp8_blockscaled.restype = ci
+        L.dg_moe_sort.argtypes = [vp, ci, i64, ci, ci, ci, i64, vp, vp, vp, vp, vp, vp]
+        L.dg_moe_sort.restype = ci
+        L.dg_moe_rows.argtypes = [i64, ci, ci, ci]
+        L.dg_moe_rows.restype = i64
+        L.dg_moe_sort_workspace.argtypes = [i64, ci, ci]
+        L.dg_moe_sort_workspace.restype = i64
+        L.dg_moe_permute.argtypes = [vp, ci, vp, vp, vp, i64, ci, i64, i64, vp]
+        L.dg_moe_permute.restype = ci
+        L.dg_moe_permute_fp8.argtypes = [vp, ci, vp, vp, ci, vp, vp, i64, ci, i64, i64, vp]
+        L.dg_moe_permute_fp8.restype = ci
+        L.dg_moe_combine.argtypes = [vp, ci, vp, vp, vp, i64, ci, i64, i64, vp]
+        L.dg_moe_combine.restype = ci
+        L.dg_moe_combine_bwd.argtypes = [vp, vp, ci, vp, vp, vp, vp, vp, i64, ci, i64, i64, vp]
+        L.dg_moe_combine_bwd.restype = ci
+        L.dg_swiglu_fp8.argtypes = [vp, ci, vp, vp, vp, vp, i64, i64, vp]
+        L.dg_swiglu_fp8.restype = ci
+        L.dg_swiglu_fp8_bwd.argtypes = [vp, ci, vp, vp, vp, i64, i64, vp]
+        L.dg_swiglu_fp8_bwd.restype = ci
+        L.dg_grouped_wgrad_fp8.argtypes = [vp, vp, vp, vp, vp, ci, i64, i64, i64, vp, ci, ci, vp]
+        L.dg_grouped_wgrad_fp8.restype = ci
         L.dg_status_string.argtypes = [ci]
         L.dg_status_string.restype = ctypes.c_char_p
         _lib = L
@@ -120,6 +148,53 @@ def dg_grouped_gemm_fp8_segments(A, a_fmt, sA, B, b_fmt, sB, C, group_offsets, n
 
 def dg_quantize_fp8_blockscaled(X, in_dtype, Q, S, M, K, block_rows, stream) -> int:
     return lib().dg_quantize_fp8_blockscaled(X, in_dtype, Q, S, M, K, block_rows, stream)
+
+
+def dg_moe_sort(ids, ids_dtype, T, top_k, num_groups, align, M_total, group_offsets, group_counts, row_slot,
+                slot_row, workspace, stream) -> int:
+    return lib().dg_moe_sort(ids, ids_dtype, T, top_k, num_groups, align, M_total, group_offsets, group_counts,
+                             row_slot, slot_row, workspace, stream)
+
+
+def dg_moe_rows(T, top_k, num_groups, align) -> int:
+    return lib().dg_moe_rows(T, top_k, num_groups, align)
+
+
+def dg_moe_sort_workspace(T, top_k, num_groups) -> int:
+    return lib().dg_moe_sort_workspace(T, top_k, num_groups)
+
+
+def dg_moe_permute(X, dtype, Y, slot_row, row_slot, T, top_k, M_total, H, stream) -> int:
+    return lib().dg_moe_permute(X, dtype, Y, slot_row, row_slot, T, top_k, M_total, H, stream)
+
+
+def dg_moe_permute_fp8(X, in_dtype, Q, S, scale_mode, slot_row, row_slot, T, top_k, M_total, H, stream) -> int:
+    return lib().dg_moe_permute_fp8(X, in_dtype, Q, S, scale_mode, slot_row, row_slot, T, top_k, M_total, H,
+                                    stream)
+
+
+def dg_moe_combine(Y, dtype, weights, slot_row, out, T, top_k, M_total, H, stream) -> int:
+    return lib().dg_moe_combine(Y, dtype, weights, slot_row, out, T, top_k, M_total, H, stream)
+
+
+def dg_moe_combine_bwd(dOut, Y, dtype, weights, slot_row, row_slot, dY, dweights, T, top_k, M_total, H,
+                       stream) -> int:
+    return lib().dg_moe_combine_bwd(dOut, Y, dtype, weights, slot_row, row_slot, dY, dweights, T, top_k, M_total,
+                                    H, stream)
+
+
+def dg_swiglu_fp8(H, in_dtype, A, sA, Hq, sH, M, I, stream) -> int:
+    return lib().dg_swiglu_fp8(H, in_dtype, A, sA, Hq, sH, M, I, stream)
+
+
+def dg_swiglu_fp8_bwd(dA, dtype, Hq, sH, dH, M, I, stream) -> int:
+    return lib().dg_swiglu_fp8_bwd(dA, dtype, Hq, sH, dH, M, I, stream)
+
+
+def dg_grouped_wgrad_fp8(dY, X, sX, group_offsets, group_counts, num_groups, M_total, N, K, dW, out_dtype,
+                         accumulate, stream) -> int:
+    return lib().dg_grouped_wgrad_fp8(dY, X, sX, group_offsets, group_counts, num_groups, M_total, N, K, dW,
+                                      out_dtype, accumulate, stream)
 
 
 def dg_status_string(status: int) -> str:
@@ -335,3 +410,242 @@ def quantize_fp8_blockscaled(X, block_rows=128, Q=None, S=None, stream=None):
     if st != DG_OK:
         raise DGError(st, "dg_quantize_fp8_blockscaled")
     return Q, S
+
+
+# ---------------------------------------------------------------- around the products
+
+class MoEPlan(NamedTuple):
+    """What moe_sort finds out about one batch (device int32 tensors)."""
+    group_offsets: object     # [G + 1] first rows of the experts' segments; the last entry is the row count
+    group_counts: object      # [G] real rows
+    row_slot: object          # [M] slot t * top_k + j of a row, -1 for padding
+    slot_row: object          # [T][top_k] row of a slot, -1 when dropped
+
+
+def _on(stream):
+    """Context in which new tensors belong to `stream` (None: the current one),
+    so that the allocator never hands out memory that other streams' pending
+    work still uses."""
+    if stream is None:
+        return contextlib.nullcontext()
+    torch = _torch()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    return torch.cuda.stream(stream)
+
+
+def _check(t, name, dtypes, shape=None):
+    """`t` is a contiguous tensor on the current device, of one of `dtypes`."""
+    torch = _torch()
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d).removeprefix('torch.') for d in dtypes)}, got {t.dtype}")
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous device tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+
+
+def _in_code(t, name):
+    torch = _torch()
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D tensor")
+    _check(t, name, (torch.bfloat16, torch.float32))
+    return DG_IN_BF16 if t.dtype == torch.bfloat16 else DG_IN_F32
+
+
+def _new_or(t, name, shape, dtype, like):
+    """The output tensor `t`, checked, or a new one."""
+    if t is None:
+        return _torch().empty(shape, dtype=dtype, device=like.device)
+    _check(t, name, (dtype,), tuple(shape))
+    return t
+
+
+def _check_plan(slot_row, row_slot, T):
+    """(top_k, M) of a plan's maps; row_slot may be None."""
+    torch = _torch()
+    if slot_row.dim() != 2 or slot_row.shape[0] != T or slot_row.shape[1] < 1:
+        raise ValueError(f"slot_row has shape {tuple(slot_row.shape)}, expected ({T}, top_k)")
+    _check(slot_row, "slot_row", (torch.int32,))
+    if row_slot is not None:
+        if row_slot.dim() != 1:
+            raise ValueError("row_slot must be a 1-D tensor")
+        _check(row_slot, "row_slot", (torch.int32,))
+    return slot_row.shape[1]
+
+
+def _done(st, what):
+    if st != DG_OK:
+        raise DGError(st, what)
+
+
+def moe_sort(ids, num_groups, align=128, rows=None, stream=None):
+    """The MoEPlan of expert ids[T][top_k] (int32 or int64; a choice whose id
+    lies outside [0, num_groups) is dropped).  align: 128 for the padded
+    segments of grouped_gemm_fp8, 1 for the packed ones of
+    grouped_gemm_fp8_segments.  rows: rows of the sorted matrix, by default the
+    most that any ids need (dg_moe_rows); nothing waits for the device."""
+    torch = _torch()
+    if ids.dim() != 2:
+        raise ValueError("ids must be [T][top_k]")
+    _check(ids, "ids", (torch.int32, torch.int64))
+    T, k = ids.shape
+    M = dg_moe_rows(T, k, num_groups, align) if rows is None else rows
+    ws = dg_moe_sort_workspace(T, k, num_groups)
+    if M < 0 or ws < 0:
+        raise DGError(DG_ERR_INVALID_ARG, "dg_moe_sort")
+    with _on(stream):
+        # one allocation; the workspace lives as long as the plan
+        buf = torch.empty(2 * num_groups + 1 + M + T * k + ws // 4, dtype=torch.int32, device=ids.device)
+        offs, counts, row_slot, slot_row, work = buf.split_with_sizes(
+            [num_groups + 1, num_groups, M, T * k, ws // 4])
+    _done(dg_moe_sort(ids.data_ptr(), DG_IDX_I64 if ids.dtype == torch.int64 else DG_IDX_I32, T, k, num_groups,
+                      align, M, offs.data_ptr(), counts.data_ptr(), row_slot.data_ptr(), slot_row.data_ptr(),
+                      work.data_ptr() if ws else None, _stream(stream)), "dg_moe_sort")
+    return MoEPlan(offs, counts, row_slot, slot_row.view(T, k))
+
+
+def moe_permute(X, slot_row, row_slot, Y=None, stream=None):
+    """Rows of X[T][H] (bfloat16 or float32) in the plan's order: Y[M][H], zeros
+    in rows of padding.  Its gradient is moe_combine without weights."""
+    code = _in_code(X, "X")
+    T, H = X.shape
+    k = _check_plan(slot_row, row_slot, T)
+    M = row_slot.shape[0]
+    with _on(stream):
+        Y = _new_or(Y, "Y", (M, H), X.dtype, X)
+    _done(dg_moe_permute(X.data_ptr(), code, Y.data_ptr(), slot_row.data_ptr(), row_slot.data_ptr(), T, k, M, H,
+                         _stream(stream)), "dg_moe_permute")
+    return Y
+
+
+def scale_code(scale) -> int:
+    if scale in (DG_SCALE_AMAX, "amax"):
+        return DG_SCALE_AMAX
+    if scale in (DG_SCALE_POW2, "pow2"):
+        return DG_SCALE_POW2
+    raise ValueError(f"unknown scale mode {scale!r}")
+
+
+def moe_permute_fp8(X, slot_row, row_slot, scale="pow2", Q=None, S=None, stream=None):
+    """The same, quantised: E4M3 codes Q[M][H] and one FP32 scale per row and 128
+    columns, S[M][ceil(H/128)] (A and sA of the grouped products).  scale:
+    "pow2" (powers of two: what grouped_wgrad_fp8 reads without rounding) or
+    "amax" (amax / 448)."""
+    torch = _torch()
+    code = _in_code(X, "X")
+    mode = scale_code(scale)
+    T, H = X.shape
+    k = _check_plan(slot_row, row_slot, T)
+    M = row_slot.shape[0]
+    with _on(stream):
+        Q = _new_or(Q, "Q", (M, H), torch.uint8, X)
+        S = _new_or(S, "S", (M, -(-H // 128)), torch.float32, X)
+    _done(dg_moe_permute_fp8(X.data_ptr(), code, Q.data_ptr(), S.data_ptr(), mode, slot_row.data_ptr(),
+                             row_slot.data_ptr(), T, k, M, H, _stream(stream)), "dg_moe_permute_fp8")
+    return Q, S
+
+
+def moe_combine(Y, slot_row, weights=None, out=None, stream=None):
+    """out[t] = sum_j weights[t][j] Y[slot_row[t][j]] (weights None: ones), of Y's
+    dtype; dropped choices add nothing."""
+    torch = _torch()
+    code = _in_code(Y, "Y")
+    M, H = Y.shape
+    T = slot_row.shape[0]
+    k = _check_plan(slot_row, None, T)
+    if weights is not None:
+        _check(weights, "weights", (torch.float32,), (T, k))
+    with _on(stream):
+        out = _new_or(out, "out", (T, H), Y.dtype, Y)
+    _done(dg_moe_combine(Y.data_ptr(), code, None if weights is None else weights.data_ptr(), slot_row.data_ptr(),
+                         out.data_ptr(), T, k, M, H, _stream(stream)), "dg_moe_combine")
+    return out
+
+
+def moe_combine_bwd(dOut, Y, slot_row, row_slot, weights, dY=None, dweights=None, stream=None):
+    """The gradient of moe_combine with weights: dY[M][H] (zeros in rows of
+    padding) and dweights[T][top_k] (float32)."""
+    torch = _torch()
+    code = _in_code(dOut, "dOut")
+    T, H = dOut.shape
+    k = _check_plan(slot_row, row_slot, T)
+    M = row_slot.shape[0]
+    _check(Y, "Y", (dOut.dtype,), (M, H))
+    _check(weights, "weights", (torch.float32,), (T, k))
+    with _on(stream):
+        dY = _new_or(dY, "dY", (M, H), dOut.dtype, dOut)
+        dweights = _new_or(dweights, "dweights", (T, k), torch.float32, dOut)
+    _done(dg_moe_combine_bwd(dOut.data_ptr(), Y.data_ptr(), code, weights.data_ptr(), slot_row.data_ptr(),
+                             row_slot.data_ptr(), dY.data_ptr(), dweights.data_ptr(), T, k, M, H, _stream(stream)),
+          "dg_moe_combine_bwd")
+    return dY, dweights
+
+
+def swiglu_fp8(H, checkpoint=True, stream=None):
+    """a = u g / (1 + exp(-g)) of H[M][2 I] = [g | u] (bfloat16 or float32) in 8
+    bits: (A[M][I], sA[M][ceil(I/128)], Hq[M][2 I], sH[M][2][ceil(I/128)]), E4M3
+    codes with power-of-two scales.  Hq, sH are H's checkpoint for
+    swiglu_fp8_bwd; None without `checkpoint`."""
+    torch = _torch()
+    code = _in_code(H, "H")
+    M, I = H.shape[0], H.shape[1] // 2
+    if H.shape[1] % 2:
+        raise ValueError("H must have an even number of columns")
+    Ib = -(-I // 128)
+    with _on(stream):
+        A = torch.empty((M, I), dtype=torch.uint8, device=H.device)
+        sA = torch.empty((M, Ib), dtype=torch.float32, device=H.device)
+        Hq = sH = None
+        if checkpoint:
+            Hq = torch.empty((M, 2 * I), dtype=torch.uint8, device=H.device)
+            sH = torch.empty((M, 2, Ib), dtype=torch.float32, device=H.device)
+    # an empty tensor's address may be null, which would ask for no checkpoint
+    _done(dg_swiglu_fp8(H.data_ptr(), code, A.data_ptr(), sA.data_ptr(), Hq.data_ptr() if checkpoint else None,
+                        sH.data_ptr() if checkpoint else None, M, I, _stream(stream)), "dg_swiglu_fp8")
+    return A, sA, Hq, sH
+
+
+def swiglu_fp8_bwd(dA, Hq, sH, dH=None, stream=None):
+    """The gradient dH[M][2 I] of swiglu_fp8 from dA[M][I] (bfloat16 or float32)
+    and the checkpoint."""
+    torch = _torch()
+    code = _in_code(dA, "dA")
+    M, I = dA.shape
+    _check(Hq, "Hq", (torch.uint8, torch.float8_e4m3fn), (M, 2 * I))
+    _check(sH, "sH", (torch.float32,), (M, 2, -(-I // 128)))
+    with _on(stream):
+        dH = _new_or(dH, "dH", (M, 2 * I), dA.dtype, dA)
+    _done(dg_swiglu_fp8_bwd(dA.data_ptr(), code, Hq.data_ptr(), sH.data_ptr(), dH.data_ptr(), M, I,
+                            _stream(stream)), "dg_swiglu_fp8_bwd")
+    return dH
+
+
+def grouped_wgrad_fp8(dY, X, sX, group_offsets, group_counts=None, out_dtype="f32", dW=None, accumulate=False,
+                      stream=None):
+    """dW[G][N][K], each expert's dY^T X over its rows, of dY[M][N] (bfloat16) and
+    8-bit activations X[M][K] with scales sX[M][ceil(K/128)].  accumulate adds to
+    dW; rows past group_counts are not used."""
+    torch = _torch()
+    if dY.dim() != 2 or X.dim() != 2 or group_offsets.dim() != 1:
+        raise ValueError("dY and X must be 2-D, group_offsets 1-D")
+    M, N = dY.shape
+    K = X.shape[1]
+    G = group_offsets.shape[0] - 1
+    _check(dY, "dY", (torch.bfloat16,))
+    _check(X, "X", (torch.uint8, torch.float8_e4m3fn), (M, K))
+    _check(sX, "sX", (torch.float32,), (M, -(-K // 128)))
+    _check(group_offsets, "group_offsets", (torch.int32,))
+    if group_counts is not None:
+        _check(group_counts, "group_counts", (torch.int32,), (G,))
+    if accumulate and dW is None:
+        raise ValueError("accumulate needs dW")
+    code = out_code(out_dtype)
+    with _on(stream):
+        dW = _new_or(dW, "dW", (G, N, K), torch.float32 if code == DG_OUT_F32 else torch.bfloat16, dY)
+    _done(dg_grouped_wgrad_fp8(dY.data_ptr(), X.data_ptr(), sX.data_ptr(), group_offsets.data_ptr(),
+                               None if group_counts is None else group_counts.data_ptr(), G, M, N, K,
+                               dW.data_ptr(), code, int(bool(accumulate)), _stream(stream)), "dg_grouped_wgrad_fp8")
+    return dW
