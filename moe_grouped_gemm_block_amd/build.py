@@ -24,7 +24,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libdg.so")
 LIB_STAGES1 = os.path.join(PKG, "libdg_stages1.so")
 SOURCES = ["dg_api.hip", "kernels_e4m3.hip", "kernels_e4m3_e5m2.hip", "kernels_e5m2_e4m3.hip",
-           "kernels_e5m2.hip", "moe_api.hip"]
+           "kernels_e5m2.hip", "kernels_wgrad.hip", "moe_api.hip"]
 ARCH = os.environ.get("DG_OFFLOAD_ARCH", "gfx950")
 HARMLESS = "packed-fp32-ops' is not a recognized feature"
 
@@ -42,7 +42,8 @@ def compile_command(src: str, obj: str, stages: int = 2) -> list[str]:
             "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
             # matrix-core results in ordinary VGPRs: the FP32 rescale reads them
             # directly instead of copying each one out of an accumulation register
-            "-mllvm", "-amdgpu-mfma-vgpr-form=1",
+            # (the weight gradient's accumulators fill all 256 of the latter)
+            "-mllvm", f"-amdgpu-mfma-vgpr-form={int(src != 'kernels_wgrad.hip')}",
             "-I", INCLUDE, "-I", CSRC, os.path.join(CSRC, src), "-o", obj]
 
 

@@ -9,6 +9,7 @@
 //   DG_DEFINE_FMT_54  E5M2 A x E4M3 B   (suffix _a5b4)
 //   DG_DEFINE_FMT_55  E5M2 A x E5M2 B   (suffix _a5b5)
 //   DG_DEFINE_MISC    the quantiser
+//   DG_DEFINE_WGRAD   the weight gradient
 // The kernel headers pass DG_KERNEL(<family>, <group>) as the macro that
 // emits each kernel: <family>_DEF (definition) or <family>_DECL (declaration).
 #pragma once
@@ -40,6 +41,11 @@
 #define DG_MODE_MISC _DEF
 #else
 #define DG_MODE_MISC _DECL
+#endif
+#ifdef DG_DEFINE_WGRAD
+#define DG_MODE_WGRAD _DEF
+#else
+#define DG_MODE_WGRAD _DECL
 #endif
 
 #define DG_KERNEL(FAMILY, GROUP) DG_CAT(FAMILY, DG_CAT(DG_MODE_, GROUP))

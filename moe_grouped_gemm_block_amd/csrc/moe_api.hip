@@ -43,8 +43,6 @@ DG_MOE_KERNEL(dg_swiglu_fp8_bf16_nockpt, 256, SwigluArgs, swiglu_body<true, fals
 DG_MOE_KERNEL(dg_swiglu_fp8_f32_nockpt, 256, SwigluArgs, swiglu_body<false, false>)
 DG_MOE_KERNEL(dg_swiglu_fp8_bwd_bf16, 256, SwigluBwdArgs, swiglu_bwd_body<true>)
 DG_MOE_KERNEL(dg_swiglu_fp8_bwd_f32, 256, SwigluBwdArgs, swiglu_bwd_body<false>)
-DG_MOE_KERNEL(dg_wgrad_fp8_bf16, 256, WgradArgs, wgrad_body<true>)
-DG_MOE_KERNEL(dg_wgrad_fp8_f32, 256, WgradArgs, wgrad_body<false>)
 #undef DG_MOE_KERNEL
 
 }  // namespace dg
@@ -254,10 +252,20 @@ int dg_grouped_wgrad_fp8(const void* dY, const void* X, const float* sX, const i
   // rows of dY and X start 16-byte aligned
   if (N % 8 != 0 || K % 16 != 0 || N > kMaxWidth || K > kMaxWidth) return DG_ERR_UNSUPPORTED;
   dg::WgradArgs a{static_cast<const uint16_t*>(dY), static_cast<const uint8_t*>(X), sX, group_offsets, group_counts,
-                  dW, num_groups, int(M_total), int(N), int(K), int(ceil_div(K, 128)), int(ceil_div(N, 128)),
-                  int(ceil_div(K, 128)), accumulate};
-  return launch(out_dtype == DG_OUT_BF16 ? dg::dg_wgrad_fp8_bf16 : dg::dg_wgrad_fp8_f32, a,
-                int64_t(num_groups) * a.n_tiles * a.k_tiles, 256, stream);
+                  dW, num_groups, int(M_total), int(N), int(K), int(ceil_div(K, 128)), 0, 0, 0, accumulate};
+  const bool bf16 = out_dtype == DG_OUT_BF16;
+  // 256 x 128 tiles from more than one per CU (256) on, 128 x 128 below (FP32,
+  // 256 x 128 against 128 x 128: 64 tiles of 1024 rows 26.1 / 20.8 us, 256 of 256
+  // rows 17.8 / 17.5, 384 of 256 rows 23.7 / 24.6, 512 of 512 rows 29.6 / 35.5)
+  const bool big = num_groups * ceil_div(N, 256) * ceil_div(K, 128) > 256;
+  a.n_tiles = int(ceil_div(N, big ? 256 : 128));
+  a.k_tiles = int(ceil_div(K, 128));
+  const int64_t tiles = int64_t(a.n_tiles) * a.k_tiles;
+  // (fewer tiles would leave XCDs without work: the last eighth may be short)
+  a.per_xcd = tiles >= 64 ? int(ceil_div(tiles, 8)) : 0;
+  return launch(big ? (bf16 ? dg::dg_wgrad256_bf16 : dg::dg_wgrad256_f32)
+                    : (bf16 ? dg::dg_wgrad128_bf16 : dg::dg_wgrad128_f32),
+                a, num_groups * (a.per_xcd ? 8 * int64_t(a.per_xcd) : tiles), 256, stream);
 }
 
 }  // extern "C"

@@ -182,6 +182,22 @@ def test_wgrad(counts, align, N, K, out):
 
 
 @pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("G,N,K", [(260, 136, 144), (65, 520, 272), (3, 2056, 1552)])
+def test_wgrad_many_tiles(G, N, K, out):
+    """More tiles than CUs, the last of each row and column partial."""
+    log(f"wgrad G={G} N={N} K={K} {out}")
+    counts = np.random.default_rng(G).integers(0, 140, G).tolist()
+    counts[0] = 0
+    offs, cnt, M, codes, scales, dy = wgrad_data(counts, 1, N, K, seed=G)
+    d = to_dev(dy, codes, scales, offs, cnt)
+    got = dg.grouped_wgrad_fp8(*d, out_dtype=out)
+    x, y = (torch.from_numpy(v) for v in (O.dequantise(codes, scales), dy.double().numpy()))
+    want = torch.stack([y[o:o + n].T @ x[o:o + n] for o, n in zip(offs, cnt)]).numpy()
+    mass = torch.stack([y[o:o + n].abs().T @ x[o:o + n].abs() for o, n in zip(offs, cnt)]).numpy()
+    check_wgrad(got, want, mass, counts, out)
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
 def test_wgrad_accumulates(out):
     counts = [40, 0, 65]
     offs, cnt, M, codes, scales, dy = wgrad_data(counts, 1, 72, 160, seed=1)
