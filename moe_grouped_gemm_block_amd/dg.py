@@ -209,9 +209,15 @@ class DGError(RuntimeError):
 
 # ---------------------------------------------------------------- torch helpers
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _check_fp8(t, name):
@@ -273,7 +279,8 @@ def fmt_code(fmt) -> int:
 
 def _stream(stream):
     if stream is None:
-        return _torch().cuda.current_stream().cuda_stream
+        # the handle alone: a Stream object around it takes 3 us, a kernel launch's time
+        return _torch()._C._cuda_getCurrentRawStream(_device())
     return getattr(stream, "cuda_stream", stream)
 
 
@@ -422,12 +429,20 @@ class MoEPlan(NamedTuple):
     slot_row: object          # [T][top_k] row of a slot, -1 when dropped
 
 
+_HERE = contextlib.nullcontext()
+
+
+def _device() -> int:
+    """The current device (torch.cuda.current_device without its own checks)."""
+    return _torch()._C._cuda_getDevice()
+
+
 def _on(stream):
     """Context in which new tensors belong to `stream` (None: the current one),
     so that the allocator never hands out memory that other streams' pending
     work still uses."""
     if stream is None:
-        return contextlib.nullcontext()
+        return _HERE
     torch = _torch()
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream))
@@ -436,15 +451,14 @@ def _on(stream):
 
 def _check(t, name, dtypes, shape=None):
     """`t` is a contiguous tensor on the current device, of one of `dtypes`."""
-    torch = _torch()
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d).removeprefix('torch.') for d in dtypes)}, got {t.dtype}")
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous device tensor")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    if t.get_device() != _device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{_device()}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
 def _in_code(t, name):
@@ -458,8 +472,8 @@ def _in_code(t, name):
 def _new_or(t, name, shape, dtype, like):
     """The output tensor `t`, checked, or a new one."""
     if t is None:
-        return _torch().empty(shape, dtype=dtype, device=like.device)
-    _check(t, name, (dtype,), tuple(shape))
+        return like.new_empty(shape, dtype=dtype)
+    _check(t, name, (dtype,), shape)
     return t
 
 
@@ -498,7 +512,7 @@ def moe_sort(ids, num_groups, align=128, rows=None, stream=None):
         raise DGError(DG_ERR_INVALID_ARG, "dg_moe_sort")
     with _on(stream):
         # one allocation; the workspace lives as long as the plan
-        buf = torch.empty(2 * num_groups + 1 + M + T * k + ws // 4, dtype=torch.int32, device=ids.device)
+        buf = ids.new_empty(2 * num_groups + 1 + M + T * k + ws // 4, dtype=torch.int32)
         offs, counts, row_slot, slot_row, work = buf.split_with_sizes(
             [num_groups + 1, num_groups, M, T * k, ws // 4])
     _done(dg_moe_sort(ids.data_ptr(), DG_IDX_I64 if ids.dtype == torch.int64 else DG_IDX_I32, T, k, num_groups,
@@ -596,12 +610,12 @@ def swiglu_fp8(H, checkpoint=True, stream=None):
         raise ValueError("H must have an even number of columns")
     Ib = -(-I // 128)
     with _on(stream):
-        A = torch.empty((M, I), dtype=torch.uint8, device=H.device)
-        sA = torch.empty((M, Ib), dtype=torch.float32, device=H.device)
+        A = H.new_empty((M, I), dtype=torch.uint8)
+        sA = H.new_empty((M, Ib), dtype=torch.float32)
         Hq = sH = None
         if checkpoint:
-            Hq = torch.empty((M, 2 * I), dtype=torch.uint8, device=H.device)
-            sH = torch.empty((M, 2, Ib), dtype=torch.float32, device=H.device)
+            Hq = H.new_empty((M, 2 * I), dtype=torch.uint8)
+            sH = H.new_empty((M, 2, Ib), dtype=torch.float32)
     # an empty tensor's address may be null, which would ask for no checkpoint
     _done(dg_swiglu_fp8(H.data_ptr(), code, A.data_ptr(), sA.data_ptr(), Hq.data_ptr() if checkpoint else None,
                         sH.data_ptr() if checkpoint else None, M, I, _stream(stream)), "dg_swiglu_fp8")
