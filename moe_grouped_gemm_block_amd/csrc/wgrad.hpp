@@ -17,12 +17,19 @@
 // steps later through registers and back as BF16, one conversion per element and
 // tile.  Copies run three steps ahead and are counted by hand.
 //
-// What bounds it: beside the products, the stores of dW.  8 experts of 1024 rows,
-// N = K = 4096, FP32: 332 us, 830 TFLOP/s (537 MB of results take 90 us by
-// themselves, further rows cost 1.25 PFLOP/s; a library product of BF16 operands
-// of this form reaches 1.23); 64 experts with 16384 rows unevenly, N = K = 2048,
-// BF16: 265 us.  A first kernel with 128 x 128 tiles, plain LDS reads and one
-// stage took 967 and 627 us, one workgroup of 256 x 256 tiles per CU 360 and 329.
+// The results leave through LDS in whole lines and past the caches (non-temporal
+// stores), which keeps the operands in L2: 8 experts of 1024 rows with FP32
+// results 333 -> 318 us, 64 uneven experts with BF16 results 277 -> 258 us
+// (non-temporal stores of half lines were slower, 353 and 295).
+//
+// What bounds it: the products and the stores of dW, which hardly overlap.  8
+// experts of 1024 rows, N = K = 4096, FP32: 315 us, 870 TFLOP/s (537 MB of
+// results take 93 us by themselves, further rows cost 1.2 to 1.3 PFLOP/s; a
+// library product of BF16 operands of this form reaches 1.23, the same loop
+// without its loads and decoding 2.1); 64 experts with 16384 rows unevenly,
+// N = K = 2048, BF16: 255 us.  A first kernel with 128 x 128 tiles, plain LDS
+// reads and one stage took 967 and 627 us, one workgroup of 256 x 256 tiles per
+// CU 360 and 329.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -77,6 +84,15 @@ __device__ __forceinline__ bool tile_of_expert(const WgradArgs& p, int& e, int& 
   return tile < tiles;
 }
 
+// Tiles run along pairs of tiles of N: what an XCD has in flight shares few
+// columns of dY, whose tiles are four times X's in bytes.
+__device__ __forceinline__ void tile_at(const WgradArgs& p, int tile, int& tn, int& tk) {
+  const int pair = tile / (2 * p.k_tiles), rest = tile - pair * 2 * p.k_tiles;
+  const bool two = 2 * pair + 1 < p.n_tiles;
+  tk = two ? rest >> 1 : rest;
+  tn = 2 * pair + (two ? rest & 1 : 0);
+}
+
 // Four values of each of 16 columns from LDS, transposed on the way: the
 // 16 lanes of a group read a 4 x 16 block (lane i: row i / 4, columns
 // 4 (i % 4) .. + 3, 8 bytes) and lane i gets column i of its four rows
@@ -114,7 +130,9 @@ __device__ __forceinline__ void wgrad_body(const WgradArgs& p) {
 
   int e, tile;
   if (!tile_of_expert(p, e, tile)) return;
-  const int n0 = tile / p.k_tiles * BN, k0 = tile % p.k_tiles * BK;
+  int tn, tk;
+  tile_at(p, tile, tn, tk);
+  const int n0 = tn * BN, k0 = tk * BK;
   int r0, r1;
   expert_rows(p, e, r0, r1);
   r0 = __builtin_amdgcn_readfirstlane(r0);
@@ -167,14 +185,11 @@ __device__ __forceinline__ void wgrad_body(const WgradArgs& p) {
   // every block of 16 in the first, 8 .. 15 in the second.  Granule b sits at
   // b ^ (r % 8), in the second plane at b ^ (r % 8) ^ 1: eight lanes that
   // store side by side, and the 8 rows x 32 bytes of a transposed read, hit
-  // distinct banks.  With a BF16 result, columns 8 a + 4 h + c of 32 (a, c < 4)
-  // trade places to 16 h + 4 a + c, which gives a lane eight consecutive output
-  // columns in MFMA tiles 2 j and 2 j + 1: 16-byte stores at the end.
+  // distinct banks.
   uint32_t x_wr[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const int blk = OUT_BF16 ? (xb & ~1) | h : xb, plane = OUT_BF16 ? xb & 1 : h;
-    x_wr[h] = uint32_t(X0 + xr * XROW + plane * (XROW / 2) + 16 * (blk ^ (xr & 7) ^ plane));
+    x_wr[h] = uint32_t(X0 + xr * XROW + h * (XROW / 2) + 16 * (xb ^ (xr & 7) ^ h));
   }
   u32x4 xraw, xdec[2];
   float xs;
@@ -184,9 +199,8 @@ __device__ __forceinline__ void wgrad_body(const WgradArgs& p) {
   };
   auto decode_word = [&](int w) {
     const uint2 d = decode4_bf16(xraw[w], xs);
-    const int half = OUT_BF16 ? w & 1 : w >> 1, at = OUT_BF16 ? w >> 1 : w & 1;
-    xdec[half][2 * at] = d.x;
-    xdec[half][2 * at + 1] = d.y;
+    xdec[w >> 1][2 * (w & 1)] = d.x;
+    xdec[w >> 1][2 * (w & 1) + 1] = d.y;
   };
   auto write_x = [&](uint32_t stage) {
     uint8_t* st = lds + stage * XB;
@@ -298,48 +312,52 @@ __device__ __forceinline__ void wgrad_body(const WgradArgs& p) {
       b = c2;
       c2 = t;
     }
-    wait_vmem();                                  // no copy outlives the workgroup
+    wait_vmem();                                  // no copy lands in LDS from here on
+    __syncthreads();
   }
 
-  // acc[j][i] of lane (q, r16): row n0 + wn + 16 i + r16, columns
-  // k0 + wk + 16 j + 4 q .. + 3, or with a BF16 result, tiles 2 j and 2 j + 1
-  // together, k0 + wk + 32 j + 8 q .. + 7
+  // acc[j][i] of lane (q, r16) is row n0 + wn + 16 i + r16, columns
+  // k0 + wk + 16 j + 4 q .. + 3.  Through LDS, 16 rows at a time in the wave's own
+  // part (granules of 16 bytes at g ^ row), so that stores write whole lines.
+  constexpr int GR = 4 * KI;                      // granules of a row
+  constexpr int V = OUT_BF16 ? 8 : 4;             // columns of a 16-byte store
+  constexpr int LR = 4 * GR / V;                  // lanes of a row
+  v4f* part = reinterpret_cast<v4f*>(lds) + wave * 16 * GR;
+  const int lrow = lane / LR, lcol = V * (lane % LR);
+  const int k = k0 + wk + lcol;
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
-    const int n = n0 + wn + 16 * i + r16;
-    if (n >= N) continue;
-    const size_t row = (size_t(e) * N + n) * K;
-    if constexpr (OUT_BF16) {
 #pragma unroll
-      for (int j = 0; j < KI; j += 2) {
-        const int k = k0 + wk + 16 * j + 8 * q;
-        if (k >= K) continue;
-        u32x4_nt* dst = reinterpret_cast<u32x4_nt*>(static_cast<uint16_t*>(p.dW) + row + k);
-        v4f v0 = acc[j][i], v1 = acc[j + 1][i];
-        if (p.accumulate) {
-          const u32x4_nt o = *dst;
+    for (int j = 0; j < KI; ++j) part[r16 * GR + ((4 * j + q) ^ r16 % GR)] = acc[j][i];
+    __builtin_amdgcn_wave_barrier();              // a wave's LDS operations keep their order
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            v0[2 * c] += __uint_as_float(o[c] << 16);
-            v0[2 * c + 1] += __uint_as_float(o[c] & 0xFFFF0000u);
-            v1[2 * c] += __uint_as_float(o[2 + c] << 16);
-            v1[2 * c + 1] += __uint_as_float(o[2 + c] & 0xFFFF0000u);
+    for (int h = 0; h < 16; h += 64 / LR) {
+      const int row = lrow + h, n = n0 + wn + 16 * i + row;
+      v4f v[V / 4];
+#pragma unroll
+      for (int c = 0; c < V / 4; ++c) v[c] = part[row * GR + ((lcol / 4 + c) ^ row % GR)];
+      if (n < N && k < K) {
+        const size_t at = (size_t(e) * N + n) * K + k;
+        if constexpr (OUT_BF16) {
+          u32x4_nt* dst = reinterpret_cast<u32x4_nt*>(static_cast<uint16_t*>(p.dW) + at);
+          if (p.accumulate) {
+            const u32x4_nt o = *dst;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              v[c / 2][2 * (c & 1)] += __uint_as_float(o[c] << 16);
+              v[c / 2][2 * (c & 1) + 1] += __uint_as_float(o[c] & 0xFFFF0000u);
+            }
           }
+          store16<true>(dst, u32x4_nt{pack_bf16x2(v[0][0], v[0][1]), pack_bf16x2(v[0][2], v[0][3]),
+                                       pack_bf16x2(v[1][0], v[1][1]), pack_bf16x2(v[1][2], v[1][3])});
+        } else {
+          v4f* dst = reinterpret_cast<v4f*>(static_cast<float*>(p.dW) + at);
+          if (p.accumulate) v[0] += *dst;
+          store16<true>(dst, __builtin_bit_cast(u32x4_nt, v[0]));
         }
-        store16<false>(dst, u32x4_nt{pack_bf16x2(v0[0], v0[1]), pack_bf16x2(v0[2], v0[3]),
-                                     pack_bf16x2(v1[0], v1[1]), pack_bf16x2(v1[2], v1[3])});
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < KI; ++j) {
-        const int k = k0 + wk + 16 * j + 4 * q;
-        if (k >= K) continue;
-        v4f* dst = reinterpret_cast<v4f*>(static_cast<float*>(p.dW) + row + k);
-        v4f v = acc[j][i];
-        if (p.accumulate) v += *dst;
-        *dst = v;
       }
     }
+    __builtin_amdgcn_wave_barrier();
   }
 }
 
