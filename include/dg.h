@@ -342,7 +342,8 @@ typedef enum {
 typedef enum {
   DG_SCALE_AMAX = 0,  /* s = fp32(amax / 448), as dg_quantize_fp8_blockscaled */
   DG_SCALE_POW2 = 1   /* s = 2^ceil(log2(amax / 448)), at least 2^-126: decoded
-                         values are exact bfloat16 values */
+                         values are bfloat16 values (normal ones from s = 2^-117
+                         on) */
 } dg_scale_mode;
 
 /*
@@ -459,7 +460,7 @@ int dg_swiglu_fp8_bwd(const void* dA, int dtype, const void* Hq, const float* sH
  *        rows)
  *
  * s dec(X) enters the products rounded to bfloat16, which changes nothing when
- * the scales are powers of two.  N a multiple of 8 and K of 16
+ * the scales are powers of two (from 2^-117 on).  N a multiple of 8 and K of 16
  * (DG_ERR_UNSUPPORTED).
  */
 int dg_grouped_wgrad_fp8(const void* dY, const void* X, const float* sX, const int32_t* group_offsets,

@@ -42,8 +42,7 @@ def compile_command(src: str, obj: str, stages: int = 2) -> list[str]:
             "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
             # matrix-core results in ordinary VGPRs: the FP32 rescale reads them
             # directly instead of copying each one out of an accumulation register
-            # (the weight gradient's accumulators fill all 256 of the latter)
-            "-mllvm", f"-amdgpu-mfma-vgpr-form={int(src != 'kernels_wgrad.hip')}",
+            "-mllvm", "-amdgpu-mfma-vgpr-form=1",
             "-I", INCLUDE, "-I", CSRC, os.path.join(CSRC, src), "-o", obj]
 
 

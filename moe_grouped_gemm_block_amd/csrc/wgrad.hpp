@@ -163,7 +163,7 @@ __device__ __forceinline__ void wgrad_body(const WgradArgs& p) {
   const int yr = wave * YR + lane / (64 / YR), yc = lane % (64 / YR);
   const uint32_t y_lane = uint32_t(yr * N + 16 * ((yc >> 1) ^ (yr & 7)) + 8 * (yc & 1)) * 2u;
   auto copy_y = [&](int s, uint32_t slot) {
-    const i32x4 rs = make_rsrc(p.dY + size_t(r0 + s * BR) * N + n0, step_size(y_size, s));
+    const i32x4 rs = make_rsrc(p.dY + (size_t(r0) + size_t(s) * BR) * N + n0, step_size(y_size, s));
 #pragma unroll
     for (int c = 0; c < YC; ++c)
       copy16_to_lds(rs, y_lane + uint32_t(c * 4 * YR * N) * 2u, lds0 + slot * YB + uint32_t(c * 4096 + wave * 1024));
@@ -176,8 +176,8 @@ __device__ __forceinline__ void wgrad_body(const WgradArgs& p) {
   const uint32_t x_lane = uint32_t(xr * K + 16 * xb);
   const uint32_t s_lane = uint32_t(xr * Kb + xb / 8) * 4u;
   auto copy_x = [&](int s, uint32_t slot) {
-    const i32x4 rx = make_rsrc(p.X + size_t(r0 + s * BR) * K + k0, step_size(x_size, s));
-    const i32x4 rs = make_rsrc(p.sX + size_t(r0 + s * BR) * Kb + k0 / 128, step_size(s_size, s));
+    const i32x4 rx = make_rsrc(p.X + (size_t(r0) + size_t(s) * BR) * K + k0, step_size(x_size, s));
+    const i32x4 rs = make_rsrc(p.sX + (size_t(r0) + size_t(s) * BR) * Kb + k0 / 128, step_size(s_size, s));
     copy16_to_lds(rx, x_lane, lds0 + R0 + slot * RB + uint32_t(wave * 1024));
     copy4_to_lds(rs, s_lane, lds0 + S0 + slot * SB + uint32_t(wave * 256));
   };
@@ -250,9 +250,9 @@ __device__ __forceinline__ void wgrad_body(const WgradArgs& p) {
     float first_s[2];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const __amdgpu_buffer_rsrc_t rx = buffer_rsrc(p.X + size_t(r0 + t * BR) * K + k0, int(step_size(x_size, t)));
+      const __amdgpu_buffer_rsrc_t rx = buffer_rsrc(p.X + (size_t(r0) + size_t(t) * BR) * K + k0, int(step_size(x_size, t)));
       const __amdgpu_buffer_rsrc_t rs =
-          buffer_rsrc(p.sX + size_t(r0 + t * BR) * Kb + k0 / 128, int(step_size(s_size, t)));
+          buffer_rsrc(p.sX + (size_t(r0) + size_t(t) * BR) * Kb + k0 / 128, int(step_size(s_size, t)));
       first[t] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, int(x_lane), 0, 0));
       first_s[t] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, int(s_lane), 0, 0));
     }
