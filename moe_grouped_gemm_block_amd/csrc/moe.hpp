@@ -216,6 +216,19 @@ __device__ __forceinline__ void zero_row_elems(void* Y, size_t row, int H, int e
   }
 }
 
+// Row and place of item (blockIdx.x WIDTH + t) where a row has `per` items (per
+// WIDTH below 2^31, t < WIDTH): two divisions in 32 bits; the one in 64 bits that
+// this stands for takes over a hundred instructions, a fifth of the gated
+// activation's.
+template <int WIDTH>
+__device__ __forceinline__ void row_and_place(int t, int per, int& row, int& place) {
+  const uint32_t d = uint32_t(per), q = blockIdx.x / d;
+  const uint32_t x = (blockIdx.x - q * d) * WIDTH + uint32_t(t);
+  const uint32_t y = x / d;
+  row = int(q * WIDTH + y);
+  place = int(x - y * d);
+}
+
 // ---- permute ----------------------------------------------------------------------
 struct PermuteArgs {
   const void* X;             // [T][H]
@@ -238,11 +251,10 @@ __device__ __forceinline__ void permute_body(const PermuteArgs& p) {
     return;
   }
   const int per = WIDE ? p.H * ELEM / 16 : p.H;               // pieces of a row
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-  const int t = int(i / per);
+  int t, c;
+  row_and_place<256>(threadIdx.x, per, t, c);
   if (t >= p.T) return;
-  const int c = int(i - (long long)t * per);
-  const V v = static_cast<const V*>(p.X)[i];
+  const V v = static_cast<const V*>(p.X)[size_t(t) * per + c];
   for (int j = 0; j < p.k; ++j) {
     const int row = p.slot_row[(long long)t * p.k + j];
     if (row >= 0 && row < p.M) static_cast<V*>(p.Y)[size_t(row) * per + c] = v;
@@ -325,9 +337,8 @@ __device__ __forceinline__ void permute_fp8_body(const PermuteArgs& p) {
                      });
     return;
   }
-  const long long blk = (long long)blockIdx.x * 32 + (threadIdx.x >> 3);
-  const int t = int(blk / p.Kb);
-  const int kb = int(blk - (long long)t * p.Kb);
+  int t, kb;
+  row_and_place<32>(threadIdx.x >> 3, p.Kb, t, kb);
   const int col = kb * 128 + 16 * (lane & 7);
   const bool in = t < p.T && col < p.H;
   Q1Buf<IN_BF16> b;
@@ -358,12 +369,12 @@ __device__ __forceinline__ void permute_fp8_body(const PermuteArgs& p) {
   }
   // scales in whole lines: the workgroup's 32 blocks of each choice side by side
   __syncthreads();
-  const long long b2 = (long long)blockIdx.x * 32 + (threadIdx.x & 31);
-  const int t2 = int(b2 / p.Kb);
+  int t2, kb2;
+  row_and_place<32>(threadIdx.x & 31, p.Kb, t2, kb2);
   if (t2 >= p.T) return;
   for (int j = threadIdx.x >> 5; j < p.k; j += 8) {
     const int row = p.slot_row[(long long)t2 * p.k + j];
-    if (row >= 0 && row < p.M) p.S[size_t(row) * p.Kb + (b2 - (long long)t2 * p.Kb)] = scale[threadIdx.x & 31];
+    if (row >= 0 && row < p.M) p.S[size_t(row) * p.Kb + kb2] = scale[threadIdx.x & 31];
   }
 }
 
@@ -376,13 +387,19 @@ struct CombineArgs {
   int T, k, M, H;
 };
 
-// V values from 16-byte pieces (V = 8 BF16 or 4 FP32) or single elements.
-template <bool BF16, int V>
+// V values from 16-byte pieces (V = 8 BF16 or 4 FP32) or single elements, NT: as
+// non-temporal loads and stores of the pieces.  Measured on operands from HBM:
+// non-temporal stores take the combine of 8192 x 2 rows of 2048 from 18.7 to 16.7
+// us and the gradient of 4096 x 2 rows of 4096 from 36.9 to 32.8 us; such loads
+// of Y as well 19.7 and 32.4 us, and 15.8 instead of 11.3 us for 1009 x 6 rows of
+// 1408, whose ends share cache lines.
+template <bool BF16, int V, bool NT = false>
 __device__ __forceinline__ void load_values(const void* src, size_t e0, float* v) {
   if constexpr (V == 1) {
     v[0] = BF16 ? bf16_to_f32(static_cast<const uint16_t*>(src)[e0]) : static_cast<const float*>(src)[e0];
   } else if constexpr (BF16) {
-    const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(src) + e0);
+    const uint16_t* at = static_cast<const uint16_t*>(src) + e0;
+    const uint4 w = NT ? load16_nt(at) : *reinterpret_cast<const uint4*>(at);
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -390,8 +407,12 @@ __device__ __forceinline__ void load_values(const void* src, size_t e0, float* v
       v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
     }
   } else {
-    const float4 w = *reinterpret_cast<const float4*>(static_cast<const float*>(src) + e0);
-    v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
+    const float* at = static_cast<const float*>(src) + e0;
+    const uint4 w = NT ? load16_nt(at) : *reinterpret_cast<const uint4*>(at);
+    v[0] = __uint_as_float(w.x);
+    v[1] = __uint_as_float(w.y);
+    v[2] = __uint_as_float(w.z);
+    v[3] = __uint_as_float(w.w);
   }
 }
 
@@ -401,11 +422,11 @@ __device__ __forceinline__ void store_values(void* dst, size_t e0, const float* 
     if constexpr (BF16) static_cast<uint16_t*>(dst)[e0] = uint16_t(bf16_bits(v[0]));
     else static_cast<float*>(dst)[e0] = v[0];
   } else if constexpr (BF16) {
-    store16<false>(static_cast<uint16_t*>(dst) + e0,
+    store16<true>(static_cast<uint16_t*>(dst) + e0,
                    u32x4_nt{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
                             pack_bf16x2(v[6], v[7])});
   } else {
-    store16<false>(static_cast<float*>(dst) + e0,
+    store16<true>(static_cast<float*>(dst) + e0,
                    u32x4_nt{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])});
   }
 }
@@ -414,11 +435,10 @@ __device__ __forceinline__ void store_values(void* dst, size_t e0, const float* 
 // choices, in FP32, rounded once.  Rows of dropped slots are not read.
 template <bool BF16, int V>
 __device__ __forceinline__ void combine_body(const CombineArgs& p) {
-  const int per = p.H / V;
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-  const int t = int(i / per);
+  int t, c;
+  row_and_place<256>(threadIdx.x, p.H / V, t, c);
   if (t >= p.T) return;
-  const int c = int(i - (long long)t * per) * V;
+  c *= V;
   float acc[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) acc[v] = 0.f;
