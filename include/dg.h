@@ -430,8 +430,9 @@ int dg_moe_combine_bwd(const void* dOut, const void* Y, int dtype, const float* 
  *   Hq : E4M3FN [M][2 I], sH float32 [M][2][Ib]: codes and scales of g and of
  *        u; both null: no checkpoint is kept
  *
- * I must be a multiple of 16 (DG_ERR_UNSUPPORTED).  Non-finite inputs give
- * unspecified codes.
+ * I must be a multiple of 16 (DG_ERR_UNSUPPORTED).  Non-finite inputs, and
+ * products u g beyond FP32's largest number, give unspecified codes in their
+ * block of 128 columns.
  */
 int dg_swiglu_fp8(const void* H, int in_dtype, void* A, float* sA, void* Hq, float* sH, int64_t M,
                   int64_t I, hipStream_t stream);

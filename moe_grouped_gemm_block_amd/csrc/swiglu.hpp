@@ -13,7 +13,7 @@
 // exact BF16 values (which the weight gradient's matrix product relies on).
 //
 // Both passes are bound by memory: forward 4 bytes in and 3 out per element
-// pair (9216 rows of 2 x 4096 in BF16: 45.2 us, 5.9 TB/s; a copy reaches 5.3),
+// pair (9216 rows of 2 x 4096 in BF16: 45.6 us, 5.9 TB/s; a copy reaches 5.3),
 // backward 4 in and 4 out (6.7 TB/s).  An 8-lane group takes one block of 128
 // columns, 16 values of g, u and a per lane in registers; the block maxima are
 // reduced by lane permutations, nothing goes through LDS.  (Eight values per
@@ -45,9 +45,11 @@ struct SwigluArgs {
 };
 
 // e^-g within 2^-22 of it: the exponent's product with log2(e) keeps its
-// rounding error as a second term (FP32's alone would cost |g| 2^-24).
-// g >= -80.
+// rounding error as a second term (FP32's alone would cost |g| 2^-24).  Gates
+// count as at least -80, where e^-g comes near FP32's end, and at most 150, where
+// it is 0 and the largest gates' exponents would overflow.
 __device__ __forceinline__ float exp_neg(float g) {
+  g = __builtin_amdgcn_fmed3f(g, -80.f, 150.f);
   constexpr float L = 1.44269504088896341f, L_LO = 1.92596299e-8f;   // log2(e) = L + L_LO
   const float hi = -g * L;
   const float lo = __builtin_fmaf(-g, L, -hi) - g * L_LO;
@@ -60,8 +62,8 @@ __device__ __forceinline__ double silu_mul_f64(float g, float u) {
   return double(u) * (gd / (1.0 + exp(-gd)));
 }
 
-// u g / (1 + e^-g) within 2^-21 for g >= -80 (results below FP32's normal range
-// aside); further down e^-g would leave FP32's range
+// u g / (1 + e^-g) within 2^-21 for g >= -80 (results outside FP32's normal range
+// aside)
 __device__ __forceinline__ float silu_mul(float g, float u) {
   return u * (g * __builtin_amdgcn_rcpf(1.f + exp_neg(g)));
 }
@@ -89,7 +91,7 @@ __device__ __forceinline__ void swiglu_body(const SwigluArgs& p) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     const float g = q1_value(bg, i), u = q1_value(bu, i);
-    a[i] = silu_mul(fmaxf(g, -80.f), u);
+    a[i] = silu_mul(g, u);
     ga = fmaxf(ga, __builtin_fabsf(g));
     ua = fmaxf(ua, __builtin_fabsf(u));
   }
@@ -103,9 +105,9 @@ __device__ __forceinline__ void swiglu_body(const SwigluArgs& p) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) aa = fmaxf(aa, __builtin_fabsf(a[i]));
   aa = group8_max(aa);
+  ga = group8_max(ga);
+  ua = group8_max(ua);
   if constexpr (CHECKPOINT) {
-    ga = group8_max(ga);
-    ua = group8_max(ua);
     float sg, su;
     const Codes16 cg = encode16<true>([&](int i) { return q1_value(bg, i); }, ga, sg);
     const Codes16 cu = encode16<true>([&](int i) { return q1_value(bu, i); }, ua, su);
@@ -119,12 +121,12 @@ __device__ __forceinline__ void swiglu_body(const SwigluArgs& p) {
     }
   }
 
-  // the scale of a's block, from the maximum in reals
+  // the scale of a's block, from the maximum in reals (which FP32 may have lost)
   int e = 0;
-  bool some = aa > 0.f, all64 = false;
+  bool some = ga > 0.f && ua > 0.f, all64 = false;
   if (some) {
     e = pow2_exponent(aa * (1.f - 0x1p-20f));
-    all64 = e < -90;                      // values near FP32's lower end: no bracket is trusted
+    all64 = aa < 0x1p-81f;                // values near FP32's lower end: no bracket is trusted
     if (all64 || e != pow2_exponent(aa * (1.f + 0x1p-20f))) {
       double md = 0.0;
 #pragma unroll 1
@@ -192,7 +194,7 @@ __device__ __forceinline__ void decode4(uint32_t w, float s, float* v) {
 // A thread takes 8 columns: 8 codes of g and of u and 8 values of dA in, 8
 // values of dg and of du out.  FP32 throughout, one rounding to the output type.
 // dA and dH past the caches (non-temporal), the codes' pieces of 8 bytes not: 9216
-// rows of 2 x 4096 in BF16 45.2 us, 6.7 TB/s (all plain 52.7, all non-temporal
+// rows of 2 x 4096 in BF16 45.4 us, 6.7 TB/s (all plain 52.7, all non-temporal
 // 47.4).
 template <bool BF16>
 __device__ __forceinline__ void swiglu_bwd_body(const SwigluBwdArgs& p) {
@@ -214,9 +216,12 @@ __device__ __forceinline__ void swiglu_bwd_body(const SwigluBwdArgs& p) {
   for (int v = 0; v < 8; v += V) load_values<BF16, V, true>(p.dA, size_t(m) * p.I + col + v, d + v);
 #pragma unroll
   for (int v = 0; v < 8; ++v) {
+    // the largest numbers' codes may round up past FP32's end
+    g[v] = __builtin_amdgcn_fmed3f(g[v], -__FLT_MAX__, __FLT_MAX__);
+    u[v] = __builtin_amdgcn_fmed3f(u[v], -__FLT_MAX__, __FLT_MAX__);
     // p = 1 / (1 + e) and 1 - p = e p, which keeps its relative precision where
     // p is near 1; below -80 p and both factors are taken as at -80 (2^-115)
-    const float e = exp_neg(fmaxf(g[v], -80.f));
+    const float e = exp_neg(g[v]);
     const float pr = __builtin_amdgcn_rcpf(1.f + e);
     const float x = g[v] * pr;
     du[v] = d[v] * x;

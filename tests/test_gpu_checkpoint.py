@@ -81,6 +81,37 @@ def test_swiglu(M, I, dtype):
     assert torch.equal(A, A2) and torch.equal(sA, sA2) and none is None and none2 is None
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_swiglu_far_gates(dtype):
+    """Gates up to the type's largest number, on both sides, forward and backward."""
+    rng = np.random.default_rng(5)
+    far = np.array([3.3e38, 2.4e38, 1e30, 1e4, 151, 149, 120, 100, 89, 87, 81, 80, 79])
+    g = rng.choice(np.concatenate([far, -far]), (26, 256))
+    u = rng.standard_normal(g.shape) * np.minimum(1, 1e3 / np.abs(g))
+    g[::2], u[::2] = np.concatenate([far, -far])[:, None][::2], rng.standard_normal((13, 256)) * 1e-3
+    h = torch.from_numpy(np.concatenate([g, u], 1)).to(DTYPE[dtype]).to(DEV)
+    A, sA, Hq, sH = dg.swiglu_fp8(h)
+    torch.cuda.synchronize()
+    hd = h.double().cpu().numpy()
+    with np.errstate(over="ignore"):
+        codes, scales = O.quantise(O.swiglu(hd[:, :256], hd[:, 256:]), True)
+    assert np.array_equal(sA.cpu().numpy(), scales)
+    assert np.array_equal(A.cpu().numpy() & 0x7F, codes & 0x7F)
+    da = torch.from_numpy(rng.standard_normal(g.shape)).to(DTYPE[dtype]).to(DEV)
+    dH = dg.swiglu_fp8_bwd(da, Hq, sH)
+    gd, ud = (O.dequantise(Hq[:, i * 256:(i + 1) * 256].cpu().numpy(), sH[:, i].cpu().numpy()) for i in (0, 1))
+    with np.errstate(over="ignore"):
+        dg_, du, mass = O.swiglu_bwd(da.double().cpu().numpy(), gd, ud)
+    half = 2.0 ** -8 if dtype == "bf16" else 0.0
+    for got, want, m in ((dH[:, :256], dg_, mass), (dH[:, 256:], du, np.abs(du))):
+        bound = half * np.abs(want) + 2.0 ** -20 * m + 2.0 ** -100 * np.maximum(1, np.abs(gd))
+        ok = np.abs(got.double().cpu().numpy() - want) <= bound
+        # beyond the type's largest number the result is infinite
+        top = float(torch.finfo(DTYPE[dtype]).max)
+        ok |= (np.abs(want) > top * (1 - 2.0 ** -8)) & np.isinf(got.double().cpu().numpy())
+        assert ok.all(), np.argwhere(~ok)[:4]
+
+
 def test_swiglu_many_values():
     """A million ordinary values: none lands on the wrong side of a border."""
     rng = np.random.default_rng(0)
@@ -245,6 +276,47 @@ def test_wgrad_is_deaf_to_the_order_of_experts():
     alone = dg.grouped_wgrad_fp8(d[0][50:].contiguous(), d[1][50:].contiguous(), d[2][50:].contiguous(),
                                  torch.tensor([0, 90], dtype=torch.int32, device=DEV))
     assert torch.equal(both[1], alone[0])
+
+
+def test_rows_past_32_bit_offsets():
+    """Operands and results whose byte offsets pass 2^32."""
+    M, I = 70001, 32768
+    h = torch.zeros(M, 2 * I, device=DEV, dtype=torch.bfloat16)
+    last = torch.randn(3, 2 * I, device=DEV).bfloat16()
+    h[-3:] = last
+    A, sA, Hq, sH = dg.swiglu_fp8(h)
+    want = dg.swiglu_fp8(last)
+    for got, w in zip((A, sA, Hq, sH), want):
+        assert torch.equal(got[-3:], w)
+    assert not A[:-3].any() and bool((sA[:-3] == 1).all())
+    da = torch.randn(3, I, device=DEV).bfloat16()
+    dA = h[:, :I].contiguous()
+    dA[-3:] = da
+    dH = dg.swiglu_fp8_bwd(dA, Hq, sH)
+    assert torch.equal(dH[-3:], dg.swiglu_fp8_bwd(da, want[2], want[3]))
+    del h, dA, A, Hq
+    # dY = dH: 2 I columns
+    x = torch.randint(0, 0x70, (M, 16), dtype=torch.uint8, device=DEV)
+    s = torch.ones(M, 1, device=DEV)
+    offs = torch.tensor([0, M - 3, M], dtype=torch.int32, device=DEV)
+    counts = torch.tensor([0, 3], dtype=torch.int32, device=DEV)
+    dW = dg.grouped_wgrad_fp8(dH, x, s, offs, counts)
+    alone = dg.grouped_wgrad_fp8(dH[-3:].contiguous(), x[-3:].contiguous(), s[-3:].contiguous(),
+                                 torch.tensor([0, 3], dtype=torch.int32, device=DEV))
+    assert torch.equal(dW[1], alone[0]) and not dW[0].any()
+
+
+def test_results_past_32_bit_offsets():
+    """The last of many experts' weight gradients lies past 2^32 bytes."""
+    G, N, K = 70, 4096, 4096
+    dy, x = torch.randn(G, N, device=DEV).bfloat16(), torch.randint(0, 0x70, (G, K), dtype=torch.uint8, device=DEV)
+    s = torch.ones(G, K // 128, device=DEV)
+    offs = torch.arange(G + 1, dtype=torch.int32, device=DEV)
+    dW = dg.grouped_wgrad_fp8(dy, x, s, offs)
+    assert dW.numel() * 4 > 1 << 32
+    xv = x.view(torch.float8_e4m3fn).float()
+    for e in (0, G - 2, G - 1):                                  # single products, exact in FP32
+        assert torch.equal(dW[e], dy[e].float()[:, None] * xv[e][None])
 
 
 def test_refusals():
