@@ -4,17 +4,20 @@
 
 Each source under csrc/ (the host side, one translation unit per pair of operand
 formats, see csrc/kernels.hpp, and the operators around the products) is compiled to an object in parallel,
-then the objects are linked into libdg.so.  Packed FP32 instructions are
+then the objects are linked into libdg.so; the torch binding of the operators around the
+products (csrc/binding.cpp, host code) becomes the extension module _dg_torch.so.  Packed FP32 instructions are
 disabled for the device code (the host pass warns that it does not know the
 feature; that warning is harmless).
 """
 from __future__ import annotations
 
 import concurrent.futures
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -23,6 +26,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libdg.so")
 LIB_STAGES1 = os.path.join(PKG, "libdg_stages1.so")
+BINDING = os.path.join(PKG, "_dg_torch.so")
 SOURCES = ["dg_api.hip", "kernels_e4m3.hip", "kernels_e4m3_e5m2.hip", "kernels_e5m2_e4m3.hip",
            "kernels_e5m2.hip", "kernels_wgrad.hip", "moe_api.hip"]
 ARCH = os.environ.get("DG_OFFLOAD_ARCH", "gfx950")
@@ -50,16 +54,27 @@ def link_command(objs: list[str], out: str) -> list[str]:
     return [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", out]
 
 
+def binding_command(out: str) -> list[str]:
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    headers = os.path.join(torch, "include")
+    return [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+            "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1", "-D_GLIBCXX_USE_CXX11_ABI=1", "-I", INCLUDE,
+            "-isystem", headers, "-isystem", os.path.join(headers, "torch", "csrc", "api", "include"),
+            "-isystem", sysconfig.get_paths()["include"], "-isystem", "/opt/rocm/include",
+            os.path.join(CSRC, "binding.cpp"), "-o", out, "-L", os.path.join(torch, "lib"),
+            "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python", "-ldl"]
+
+
 def _run(cmd: list[str]) -> str:
     res = subprocess.run(cmd, capture_output=True, text=True)
     errs = "\n".join(l for l in res.stderr.splitlines() if HARMLESS not in l)
     if res.returncode != 0:
-        raise RuntimeError(f"hipcc failed ({res.returncode}): {' '.join(cmd)}\n{errs}")
+        raise RuntimeError(f"compiler failed ({res.returncode}): {' '.join(cmd)}\n{errs}")
     return errs
 
 
 def build(verbose: bool = True) -> str:
-    """Build libdg.so and its single-stage twin libdg_stages1.so (the same
+    """Build the torch binding _dg_torch.so, libdg.so and its single-stage twin libdg_stages1.so (the same
     library compiled with -DDG_STAGES=1: every GEMM pipeline with one LDS
     stage, a debugging aid whose results must equal libdg.so's bit for bit);
     returns the path of libdg.so."""
@@ -68,7 +83,7 @@ def build(verbose: bool = True) -> str:
         for stages, lib in ((2, LIB), (1, LIB_STAGES1)):
             objs = [os.path.join(tmp, f"s{stages}_" + os.path.splitext(s)[0] + ".o") for s in SOURCES]
             jobs_list.append((lib, objs, [compile_command(s, o, stages) for s, o in zip(SOURCES, objs)]))
-        cmds = [c for _, _, cs in jobs_list for c in cs]
+        cmds = [c for _, _, cs in jobs_list for c in cs] + [binding_command(BINDING + ".tmp")]
         if verbose:
             for c in cmds:
                 print(" ".join(c), flush=True)
@@ -79,7 +94,7 @@ def build(verbose: bool = True) -> str:
             warnings.append(_run(link_command(objs, lib + ".tmp")))
     if verbose and any(w.strip() for w in warnings):
         print("\n".join(w for w in warnings if w.strip()), file=sys.stderr)
-    for lib, _, _ in jobs_list:
+    for lib in [lib for lib, _, _ in jobs_list] + [BINDING]:
         os.replace(lib + ".tmp", lib)
     return LIB
 

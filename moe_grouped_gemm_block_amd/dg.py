@@ -4,14 +4,14 @@ The functions named like the C entry points take raw integers (device
 addresses, sizes, a hipStream_t handle) and return the dg_status code.  The
 torch-facing helpers below them only check dtypes / shapes / devices, pass
 ``data_ptr()`` values and the current stream, and raise on a non-zero status;
-every step of the computation runs in the library's HIP kernels.
+every step of the computation runs in the library's HIP kernels.  For the
+mixture-of-experts operators that part is native code (_dg_torch).
 
 Loading fails loudly when the library has not been built: there is no
 fallback implementation.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import NamedTuple
@@ -209,15 +209,9 @@ class DGError(RuntimeError):
 
 # ---------------------------------------------------------------- torch helpers
 
-_torch_module = None
-
-
 def _torch():
-    global _torch_module
-    if _torch_module is None:
-        import torch
-        _torch_module = torch
-    return _torch_module
+    import torch
+    return torch
 
 
 def _check_fp8(t, name):
@@ -279,8 +273,7 @@ def fmt_code(fmt) -> int:
 
 def _stream(stream):
     if stream is None:
-        # the handle alone: a Stream object around it takes 3 us, a kernel launch's time
-        return _torch()._C._cuda_getCurrentRawStream(_device())
+        return _torch().cuda.current_stream().cuda_stream
     return getattr(stream, "cuda_stream", stream)
 
 
@@ -420,6 +413,9 @@ def quantize_fp8_blockscaled(X, block_rows=128, Q=None, S=None, stream=None):
 
 
 # ---------------------------------------------------------------- around the products
+#
+# Checks of the tensors, output tensors and the current stream are native code
+# (csrc/binding.cpp, the module _dg_torch), which then makes the calls above.
 
 class MoEPlan(NamedTuple):
     """What moe_sort finds out about one batch (device int32 tensors)."""
@@ -429,71 +425,41 @@ class MoEPlan(NamedTuple):
     slot_row: object          # [T][top_k] row of a slot, -1 when dropped
 
 
-_HERE = contextlib.nullcontext()
+_binding = None
 
 
-def _device() -> int:
-    """The current device (torch.cuda.current_device without its own checks)."""
-    return _torch()._C._cuda_getDevice()
+def binding():
+    """The native binding, loaded on first use; raise if it is missing."""
+    global _binding
+    if _binding is None:
+        lib()                                     # torch's HIP runtime first, see there
+        _torch()
+        try:
+            from . import _dg_torch
+        except ImportError as e:
+            raise RuntimeError(f"{_PKG}/_dg_torch.so cannot be loaded ({e}); "
+                               f"run `python -m moe_grouped_gemm_block_amd.build` on a machine with ROCm") from e
+        _dg_torch.load(LIB_PATH, DGError)
+        _binding = _dg_torch
+    return _binding
 
 
 def _on(stream):
-    """Context in which new tensors belong to `stream` (None: the current one),
-    so that the allocator never hands out memory that other streams' pending
-    work still uses."""
-    if stream is None:
-        return _HERE
+    """Context in which `stream` (a Stream or its handle) is the current one:
+    new tensors then belong to it, so that the allocator never hands out memory
+    that other streams' pending work still uses."""
     torch = _torch()
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream))
     return torch.cuda.stream(stream)
 
 
-def _check(t, name, dtypes, shape=None):
-    """`t` is a contiguous tensor on the current device, of one of `dtypes`."""
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} must be {' or '.join(str(d).removeprefix('torch.') for d in dtypes)}, got {t.dtype}")
-    if not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous device tensor")
-    if t.get_device() != _device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{_device()}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-
-
-def _in_code(t, name):
-    torch = _torch()
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be a 2-D tensor")
-    _check(t, name, (torch.bfloat16, torch.float32))
-    return DG_IN_BF16 if t.dtype == torch.bfloat16 else DG_IN_F32
-
-
-def _new_or(t, name, shape, dtype, like):
-    """The output tensor `t`, checked, or a new one."""
-    if t is None:
-        return like.new_empty(*shape, dtype=dtype)      # 0.2 us less than with a tuple
-    _check(t, name, (dtype,), shape)
-    return t
-
-
-def _check_plan(slot_row, row_slot, T):
-    """top_k of a plan's maps; row_slot may be None."""
-    i32 = (_torch().int32,)
-    shape = slot_row.shape
-    if len(shape) != 2 or shape[0] != T or shape[1] < 1:
-        raise ValueError(f"slot_row has shape {tuple(shape)}, expected ({T}, top_k)")
-    _check(slot_row, "slot_row", i32)
-    if row_slot is not None:
-        if row_slot.dim() != 1:
-            raise ValueError("row_slot must be a 1-D tensor")
-        _check(row_slot, "row_slot", i32)
-    return shape[1]
-
-
-def _done(st, what):
-    if st != DG_OK:
-        raise DGError(st, what)
+def _call(name, stream, *args):
+    f = getattr(_binding or binding(), name)
+    if stream is None:
+        return f(*args)
+    with _on(stream):
+        return f(*args)
 
 
 def moe_sort(ids, num_groups, align=128, rows=None, stream=None):
@@ -502,38 +468,13 @@ def moe_sort(ids, num_groups, align=128, rows=None, stream=None):
     segments of grouped_gemm_fp8, 1 for the packed ones of
     grouped_gemm_fp8_segments.  rows: rows of the sorted matrix, by default the
     most that any ids need (dg_moe_rows); nothing waits for the device."""
-    torch = _torch()
-    if ids.dim() != 2:
-        raise ValueError("ids must be [T][top_k]")
-    _check(ids, "ids", (torch.int32, torch.int64))
-    T, k = ids.shape
-    M = dg_moe_rows(T, k, num_groups, align) if rows is None else rows
-    ws = dg_moe_sort_workspace(T, k, num_groups)
-    if M < 0 or ws < 0:
-        raise DGError(DG_ERR_INVALID_ARG, "dg_moe_sort")
-    with _on(stream):
-        # one allocation; the workspace lives as long as the plan
-        buf = ids.new_empty(2 * num_groups + 1 + M + T * k + ws // 4, dtype=torch.int32)
-        offs, counts, row_slot, slot_row, work = buf.split_with_sizes(
-            [num_groups + 1, num_groups, M, T * k, ws // 4])
-    _done(dg_moe_sort(ids.data_ptr(), DG_IDX_I64 if ids.dtype == torch.int64 else DG_IDX_I32, T, k, num_groups,
-                      align, M, offs.data_ptr(), counts.data_ptr(), row_slot.data_ptr(), slot_row.data_ptr(),
-                      work.data_ptr() if ws else None, _stream(stream)), "dg_moe_sort")
-    return MoEPlan(offs, counts, row_slot, slot_row.view(T, k))
+    return MoEPlan(*_call("moe_sort", stream, ids, num_groups, align, rows))
 
 
 def moe_permute(X, slot_row, row_slot, Y=None, stream=None):
     """Rows of X[T][H] (bfloat16 or float32) in the plan's order: Y[M][H], zeros
     in rows of padding.  Its gradient is moe_combine without weights."""
-    code = _in_code(X, "X")
-    T, H = X.shape
-    k = _check_plan(slot_row, row_slot, T)
-    M = row_slot.shape[0]
-    with _on(stream):
-        Y = _new_or(Y, "Y", (M, H), X.dtype, X)
-    _done(dg_moe_permute(X.data_ptr(), code, Y.data_ptr(), slot_row.data_ptr(), row_slot.data_ptr(), T, k, M, H,
-                         _stream(stream)), "dg_moe_permute")
-    return Y
+    return _call("moe_permute", stream, X, slot_row, row_slot, Y)
 
 
 def scale_code(scale) -> int:
@@ -549,54 +490,19 @@ def moe_permute_fp8(X, slot_row, row_slot, scale="pow2", Q=None, S=None, stream=
     columns, S[M][ceil(H/128)] (A and sA of the grouped products).  scale:
     "pow2" (powers of two: what grouped_wgrad_fp8 reads without rounding) or
     "amax" (amax / 448)."""
-    torch = _torch()
-    code = _in_code(X, "X")
-    mode = scale_code(scale)
-    T, H = X.shape
-    k = _check_plan(slot_row, row_slot, T)
-    M = row_slot.shape[0]
-    with _on(stream):
-        Q = _new_or(Q, "Q", (M, H), torch.uint8, X)
-        S = _new_or(S, "S", (M, -(-H // 128)), torch.float32, X)
-    _done(dg_moe_permute_fp8(X.data_ptr(), code, Q.data_ptr(), S.data_ptr(), mode, slot_row.data_ptr(),
-                             row_slot.data_ptr(), T, k, M, H, _stream(stream)), "dg_moe_permute_fp8")
-    return Q, S
+    return _call("moe_permute_fp8", stream, X, slot_row, row_slot, scale_code(scale), Q, S)
 
 
 def moe_combine(Y, slot_row, weights=None, out=None, stream=None):
     """out[t] = sum_j weights[t][j] Y[slot_row[t][j]] (weights None: ones), of Y's
     dtype; dropped choices add nothing."""
-    torch = _torch()
-    code = _in_code(Y, "Y")
-    M, H = Y.shape
-    T = slot_row.shape[0]
-    k = _check_plan(slot_row, None, T)
-    if weights is not None:
-        _check(weights, "weights", (torch.float32,), (T, k))
-    with _on(stream):
-        out = _new_or(out, "out", (T, H), Y.dtype, Y)
-    _done(dg_moe_combine(Y.data_ptr(), code, None if weights is None else weights.data_ptr(), slot_row.data_ptr(),
-                         out.data_ptr(), T, k, M, H, _stream(stream)), "dg_moe_combine")
-    return out
+    return _call("moe_combine", stream, Y, slot_row, weights, out)
 
 
 def moe_combine_bwd(dOut, Y, slot_row, row_slot, weights, dY=None, dweights=None, stream=None):
     """The gradient of moe_combine with weights: dY[M][H] (zeros in rows of
     padding) and dweights[T][top_k] (float32)."""
-    torch = _torch()
-    code = _in_code(dOut, "dOut")
-    T, H = dOut.shape
-    k = _check_plan(slot_row, row_slot, T)
-    M = row_slot.shape[0]
-    _check(Y, "Y", (dOut.dtype,), (M, H))
-    _check(weights, "weights", (torch.float32,), (T, k))
-    with _on(stream):
-        dY = _new_or(dY, "dY", (M, H), dOut.dtype, dOut)
-        dweights = _new_or(dweights, "dweights", (T, k), torch.float32, dOut)
-    _done(dg_moe_combine_bwd(dOut.data_ptr(), Y.data_ptr(), code, weights.data_ptr(), slot_row.data_ptr(),
-                             row_slot.data_ptr(), dY.data_ptr(), dweights.data_ptr(), T, k, M, H, _stream(stream)),
-          "dg_moe_combine_bwd")
-    return dY, dweights
+    return _call("moe_combine_bwd", stream, dOut, Y, slot_row, row_slot, weights, dY, dweights)
 
 
 def swiglu_fp8(H, checkpoint=True, stream=None):
@@ -604,38 +510,13 @@ def swiglu_fp8(H, checkpoint=True, stream=None):
     bits: (A[M][I], sA[M][ceil(I/128)], Hq[M][2 I], sH[M][2][ceil(I/128)]), E4M3
     codes with power-of-two scales.  Hq, sH are H's checkpoint for
     swiglu_fp8_bwd; None without `checkpoint`."""
-    torch = _torch()
-    code = _in_code(H, "H")
-    M, I = H.shape[0], H.shape[1] // 2
-    if H.shape[1] % 2:
-        raise ValueError("H must have an even number of columns")
-    Ib = -(-I // 128)
-    with _on(stream):
-        A = H.new_empty(M, I, dtype=torch.uint8)
-        sA = H.new_empty(M, Ib, dtype=torch.float32)
-        Hq = sH = None
-        if checkpoint:
-            Hq = H.new_empty(M, 2 * I, dtype=torch.uint8)
-            sH = H.new_empty(M, 2, Ib, dtype=torch.float32)
-    # an empty tensor's address may be null, which would ask for no checkpoint
-    _done(dg_swiglu_fp8(H.data_ptr(), code, A.data_ptr(), sA.data_ptr(), Hq.data_ptr() if checkpoint else None,
-                        sH.data_ptr() if checkpoint else None, M, I, _stream(stream)), "dg_swiglu_fp8")
-    return A, sA, Hq, sH
+    return _call("swiglu_fp8", stream, H, checkpoint)
 
 
 def swiglu_fp8_bwd(dA, Hq, sH, dH=None, stream=None):
     """The gradient dH[M][2 I] of swiglu_fp8 from dA[M][I] (bfloat16 or float32)
     and the checkpoint."""
-    torch = _torch()
-    code = _in_code(dA, "dA")
-    M, I = dA.shape
-    _check(Hq, "Hq", (torch.uint8, torch.float8_e4m3fn), (M, 2 * I))
-    _check(sH, "sH", (torch.float32,), (M, 2, -(-I // 128)))
-    with _on(stream):
-        dH = _new_or(dH, "dH", (M, 2 * I), dA.dtype, dA)
-    _done(dg_swiglu_fp8_bwd(dA.data_ptr(), code, Hq.data_ptr(), sH.data_ptr(), dH.data_ptr(), M, I,
-                            _stream(stream)), "dg_swiglu_fp8_bwd")
-    return dH
+    return _call("swiglu_fp8_bwd", stream, dA, Hq, sH, dH)
 
 
 def grouped_wgrad_fp8(dY, X, sX, group_offsets, group_counts=None, out_dtype="f32", dW=None, accumulate=False,
@@ -643,24 +524,5 @@ def grouped_wgrad_fp8(dY, X, sX, group_offsets, group_counts=None, out_dtype="f3
     """dW[G][N][K], each expert's dY^T X over its rows, of dY[M][N] (bfloat16) and
     8-bit activations X[M][K] with scales sX[M][ceil(K/128)].  accumulate adds to
     dW; rows past group_counts are not used."""
-    torch = _torch()
-    if dY.dim() != 2 or X.dim() != 2 or group_offsets.dim() != 1:
-        raise ValueError("dY and X must be 2-D, group_offsets 1-D")
-    M, N = dY.shape
-    K = X.shape[1]
-    G = group_offsets.shape[0] - 1
-    _check(dY, "dY", (torch.bfloat16,))
-    _check(X, "X", (torch.uint8, torch.float8_e4m3fn), (M, K))
-    _check(sX, "sX", (torch.float32,), (M, -(-K // 128)))
-    _check(group_offsets, "group_offsets", (torch.int32,))
-    if group_counts is not None:
-        _check(group_counts, "group_counts", (torch.int32,), (G,))
-    if accumulate and dW is None:
-        raise ValueError("accumulate needs dW")
-    code = out_code(out_dtype)
-    with _on(stream):
-        dW = _new_or(dW, "dW", (G, N, K), torch.float32 if code == DG_OUT_F32 else torch.bfloat16, dY)
-    _done(dg_grouped_wgrad_fp8(dY.data_ptr(), X.data_ptr(), sX.data_ptr(), group_offsets.data_ptr(),
-                               None if group_counts is None else group_counts.data_ptr(), G, M, N, K,
-                               dW.data_ptr(), code, int(bool(accumulate)), _stream(stream)), "dg_grouped_wgrad_fp8")
-    return dW
+    return _call("grouped_wgrad_fp8", stream, dY, X, sX, group_offsets, group_counts, out_code(out_dtype), dW,
+                 accumulate)

@@ -132,3 +132,17 @@ def test_helpers_refuse_host_tensors_and_wrong_types():
         dg.scale_code("e8m0")
     with pytest.raises(ValueError):
         dg.grouped_wgrad_fp8(f[0], f, f, i[0])
+
+
+def test_binding_refuses_what_is_not_a_tensor_or_a_number():
+    f, i = torch.zeros(4, 32), torch.zeros(4, 2, dtype=torch.int32)
+    for call in (lambda: dg.moe_sort([[0, 1]], 4), lambda: dg.moe_permute(f, None, i), lambda: dg.moe_combine(3, i),
+                 lambda: dg.swiglu_fp8(None), lambda: dg.grouped_wgrad_fp8(f, f, f, "offsets")):
+        with pytest.raises(TypeError):
+            call()
+    with pytest.raises(TypeError):
+        dg.binding().moe_sort(i)                                # too few arguments
+    with pytest.raises(TypeError):
+        dg.moe_sort(i.float(), 4)
+    with pytest.raises(ValueError):
+        dg.grouped_wgrad_fp8(f, f, f, i[0], out_dtype="f16")
