@@ -22,14 +22,19 @@
 // results 333 -> 318 us, 64 uneven experts with BF16 results 277 -> 258 us
 // (non-temporal stores of half lines were slower, 353 and 295).
 //
-// What bounds it: the products and the stores of dW, which hardly overlap.  8
-// experts of 1024 rows, N = K = 4096, FP32: 315 us, 870 TFLOP/s (537 MB of
-// results take 93 us by themselves, further rows cost 1.2 to 1.3 PFLOP/s; a
-// library product of BF16 operands of this form reaches 1.23, the same loop
-// without its loads and decoding 2.1); 64 experts with 16384 rows unevenly,
-// N = K = 2048, BF16: 255 us.  A first kernel with 128 x 128 tiles, plain LDS
-// reads and one stage took 967 and 627 us, one workgroup of 256 x 256 tiles per
-// CU 360 and 329.
+// What bounds it: power.  8 experts of 1024 rows, N = K = 4096, FP32: 312 us, 880
+// TFLOP/s, with the clock down to 2.0 GHz; the 537 MB of results take 93 us by
+// themselves, further rows cost 1.2 to 1.3 PFLOP/s, and a workgroup made to wait
+// between its stores, or made to start later, changes nothing (a library product
+// of BF16 operands of this form reaches 1.23 PFLOP/s, zeros in place of random
+// operands 1.46, the matrix cores alone with operands in registers 2.0).  64
+// experts with 16384 rows unevenly, N = K = 2048, BF16: 250 us at 2.25 GHz, most
+// tiles having two to eight steps: the first loads and the stores of a tile,
+// covered by one other workgroup only.  What was slower: 128 x 128 tiles, plain
+// LDS reads and one stage 967 and 627 us; one workgroup of 256 x 256 tiles per CU
+// 360 and 329; 512 workgroups that go through shares of the tiles, loading the next
+// one before the stores of the last, 329 and 304 (where rows are even, 134 instead
+// of 151 us for 256 each); the experts in order of their rows, the same on average.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -303,7 +308,6 @@ __device__ __forceinline__ void wgrad_body(const WgradArgs& p) {
           copy_x(s + 5, c2);
           copy_y(s + 3, a);
         }
-        __builtin_amdgcn_sched_barrier(0);
       }
       wait_vmem_n<G>();                           // dY of step s + 2; behind it X of s + 5 and dY of s + 3
       __syncthreads();
