@@ -120,6 +120,14 @@ Tensor output(PyObject* o, const char* name, at::IntArrayRef shape, ScalarType d
   return t;
 }
 
+// Elements [at, at + the sizes' product) of `whole` as a tensor of their own.
+Tensor part(const Tensor& whole, int64_t at, at::IntArrayRef sizes) {
+  Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(whole.storage()), whole.key_set(), whole.dtype());
+  t.unsafeGetTensorImpl()->set_storage_offset(at);
+  t.unsafeGetTensorImpl()->set_sizes_contiguous(sizes);
+  return t;
+}
+
 int64_t integer(PyObject* o, const char* name) {
   const long long v = PyLong_AsLongLong(o);
   if (v == -1 && PyErr_Occurred()) {
@@ -186,13 +194,14 @@ PyObject* moe_sort(PyObject*, PyObject* const* a, Py_ssize_t n) {
   int64_t M = k > INT32_MAX ? -1 : lib.moe_rows(T, int(k), G, align);
   if (a[3] != Py_None && M >= 0) M = integer(a[3], "rows");
   if (M < 0 || ws < 0) return failure(DG_ERR_INVALID_ARG, "dg_moe_sort");
-  const auto i32 = ids.options().dtype(at::kInt);
-  const Tensor offs = at::empty({G + 1}, i32), counts = at::empty({G}, i32);
-  const Tensor row_slot = at::empty({M}, i32), slot_row = at::empty({T, k}, i32);
-  const Tensor work = ws ? at::empty({ws / 4}, i32) : Tensor();
+  // one allocation for the plan and the workspace: four cost 2 us more
+  const Tensor all = at::empty({2 * int64_t(G) + 1 + M + T * k + ws / 4}, ids.options().dtype(at::kInt));
+  const Tensor offs = part(all, 0, {G + 1}), counts = part(all, G + 1, {G});
+  const Tensor row_slot = part(all, 2 * int64_t(G) + 1, {M}), slot_row = part(all, 2 * int64_t(G) + 1 + M, {T, k});
+  void* work = ws ? data<int32_t>(all) + 2 * int64_t(G) + 1 + M + T * k : nullptr;
   const int st = lib.moe_sort(ids.data_ptr(), ids.scalar_type() == at::kLong ? DG_IDX_I64 : DG_IDX_I32, T, int(k), G,
                               align, M, data<int32_t>(offs), data<int32_t>(counts), data<int32_t>(row_slot),
-                              data<int32_t>(slot_row), ws ? work.data_ptr() : nullptr, stream());
+                              data<int32_t>(slot_row), work, stream());
   if (st != DG_OK) return failure(st, "dg_moe_sort");
   return tuple(offs, counts, row_slot, slot_row);
   END_HANDLE_TH_ERRORS
