@@ -81,9 +81,12 @@ def log(*a):
 
 
 def kernel_source_hash() -> str:
-    """Hash of the kernel sources and of the build script (its compiler flags shape the code)."""
+    """Hash of the products' and the quantiser's kernel sources and of the build script (its
+    compiler flags shape the code); the operators around the products are not measured here."""
     h = hashlib.sha256()
-    files = sorted(glob.glob(os.path.join(ROOT, "moe_grouped_gemm_block_amd", "csrc", "*")))
+    around = {"binding.cpp", "kernels_wgrad.hip", "moe.hpp", "moe_api.hip", "swiglu.hpp", "wgrad.hpp"}
+    files = sorted(f for f in glob.glob(os.path.join(ROOT, "moe_grouped_gemm_block_amd", "csrc", "*"))
+                   if os.path.basename(f) not in around)
     files.append(os.path.join(ROOT, "moe_grouped_gemm_block_amd", "build.py"))
     for f in files:
         h.update(os.path.basename(f).encode())
