@@ -3,6 +3,7 @@
 // the same names call these; in Python the same checks and allocations take as
 // long again as the kernel launch (combine: 7.6 us a call, here 3.8).
 #include <ATen/ATen.h>
+#include <ATen/hip/EmptyTensor.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 #include <dlfcn.h>
@@ -112,9 +113,14 @@ int64_t check_rows(const Tensor& row_slot) {
   return row_slot.size(0);
 }
 
+// A new tensor on `like`'s device (at::empty without its dispatch, 0.3 us).
+Tensor create(at::IntArrayRef shape, ScalarType dtype, const Tensor& like) {
+  return at::detail::empty_cuda(shape, dtype, like.device(), c10::nullopt);
+}
+
 // The output `o`, checked, or a new tensor.
 Tensor output(PyObject* o, const char* name, at::IntArrayRef shape, ScalarType dtype, const Tensor& like) {
-  if (o == nullptr || o == Py_None) return at::empty(shape, like.options().dtype(dtype));
+  if (o == nullptr || o == Py_None) return create(shape, dtype, like);
   const Tensor& t = tensor(o, name);
   check(t, name, {dtype}, shape);
   return t;
@@ -195,7 +201,7 @@ PyObject* moe_sort(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (a[3] != Py_None && M >= 0) M = integer(a[3], "rows");
   if (M < 0 || ws < 0) return failure(DG_ERR_INVALID_ARG, "dg_moe_sort");
   // one allocation for the plan and the workspace: four cost 2 us more
-  const Tensor all = at::empty({2 * int64_t(G) + 1 + M + T * k + ws / 4}, ids.options().dtype(at::kInt));
+  const Tensor all = create({2 * int64_t(G) + 1 + M + T * k + ws / 4}, at::kInt, ids);
   const Tensor offs = part(all, 0, {G + 1}), counts = part(all, G + 1, {G});
   const Tensor row_slot = part(all, 2 * int64_t(G) + 1, {M}), slot_row = part(all, 2 * int64_t(G) + 1 + M, {T, k});
   void* work = ws ? data<int32_t>(all) + 2 * int64_t(G) + 1 + M + T * k : nullptr;
@@ -294,12 +300,11 @@ PyObject* swiglu_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (checkpoint < 0) return nullptr;
   if (H.size(1) % 2) value_error("H must have an even number of columns");
   const int64_t M = H.size(0), I = H.size(1) / 2, Ib = (I + 127) / 128;
-  const auto u8 = H.options().dtype(at::kByte), f32 = H.options().dtype(at::kFloat);
-  const Tensor A = at::empty({M, I}, u8), sA = at::empty({M, Ib}, f32);
+  const Tensor A = create({M, I}, at::kByte, H), sA = create({M, Ib}, at::kFloat, H);
   Tensor Hq, sH;
   if (checkpoint) {
-    Hq = at::empty({M, 2 * I}, u8);
-    sH = at::empty({M, 2, Ib}, f32);
+    Hq = create({M, 2 * I}, at::kByte, H);
+    sH = create({M, 2, Ib}, at::kFloat, H);
   }
   // an empty checkpoint's addresses are null, which would ask for none: no work either way
   const int st = lib.swiglu_fp8(H.data_ptr(), code, A.data_ptr(), data<float>(sA), checkpoint ? Hq.data_ptr() : nullptr,
