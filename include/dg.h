@@ -461,8 +461,8 @@ int dg_swiglu_fp8_bwd(const void* dA, int dtype, const void* Hq, const float* sH
  *        rows)
  *
  * s dec(X) enters the products rounded to bfloat16, which changes nothing when
- * the scales are powers of two (from 2^-117 on).  N a multiple of 8 and K of 16
- * (DG_ERR_UNSUPPORTED).
+ * the scales are powers of two (from 2^-117 on).  N a multiple of 8 and K of 16,
+ * and at most 2^23 tiles of 128 x 128 results (DG_ERR_UNSUPPORTED).
  */
 int dg_grouped_wgrad_fp8(const void* dY, const void* X, const float* sX, const int32_t* group_offsets,
                          const int32_t* group_counts, int num_groups, int64_t M_total, int64_t N,

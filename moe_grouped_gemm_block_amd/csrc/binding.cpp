@@ -199,7 +199,7 @@ PyObject* moe_sort(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int64_t ws = k > INT32_MAX ? -1 : lib.moe_sort_workspace(T, int(k), G);
   int64_t M = k > INT32_MAX ? -1 : lib.moe_rows(T, int(k), G, align);
   if (a[3] != Py_None && M >= 0) M = integer(a[3], "rows");
-  if (M < 0 || ws < 0) return failure(DG_ERR_INVALID_ARG, "dg_moe_sort");
+  if (M < 0 || M > INT32_MAX || ws < 0) return failure(DG_ERR_INVALID_ARG, "dg_moe_sort");
   // one allocation for the plan and the workspace: four cost 2 us more
   const Tensor all = create({2 * int64_t(G) + 1 + M + T * k + ws / 4}, at::kInt, ids);
   const Tensor offs = part(all, 0, {G + 1}), counts = part(all, G + 1, {G});

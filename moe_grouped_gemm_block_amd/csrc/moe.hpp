@@ -64,8 +64,9 @@ __device__ __forceinline__ int slot_expert(const SortArgs& p, int s) {
   return v >= 0 && v < ID(p.G) ? int(v) : -1;
 }
 
-__device__ __forceinline__ void fill_rows(int32_t* dst, int n, int first, int stride) {
-  for (int i = first; i < n; i += stride) dst[i] = -1;
+// (unsigned: one stride past n may lie past 2^31)
+__device__ __forceinline__ void fill_rows(int32_t* dst, uint32_t n, uint32_t first, uint32_t stride) {
+  for (uint32_t i = first; i < n; i += stride) dst[i] = -1;
 }
 
 template <typename ID>
@@ -189,6 +190,13 @@ __device__ __forceinline__ void sort_place_body(const SortArgs& p) {
   }
 }
 
+// ---- grids ------------------------------------------------------------------------
+// A grid has below 2^32 work-items along x, which matrices past 8 GB reach (a
+// thread per element at odd widths): more than 2^kGridBits workgroups are launched
+// as rows of that many, the last row whole.
+constexpr int kGridBits = 23;
+__device__ __forceinline__ uint32_t block_index() { return (blockIdx.y << kGridBits) + blockIdx.x; }
+
 // ---- rows of padding --------------------------------------------------------------
 // Sixteen rows per wave; `zero(r)` is called by the whole wave for each row
 // without a slot.
@@ -216,16 +224,16 @@ __device__ __forceinline__ void zero_row_elems(void* Y, size_t row, int H, int e
   }
 }
 
-// Row and place of item (blockIdx.x WIDTH + t) where a row has `per` items (per
+// Row and place of item (block_index() WIDTH + t) where a row has `per` items (per
 // WIDTH below 2^31, t < WIDTH): two divisions in 32 bits; the one in 64 bits that
 // this stands for takes over a hundred instructions, a fifth of the gated
-// activation's.
+// activation's.  Past 2^31 - 1, behind every row, the row stays there.
 template <int WIDTH>
 __device__ __forceinline__ void row_and_place(int t, int per, int& row, int& place) {
-  const uint32_t d = uint32_t(per), q = blockIdx.x / d;
-  const uint32_t x = (blockIdx.x - q * d) * WIDTH + uint32_t(t);
+  const uint32_t d = uint32_t(per), b = block_index(), q = b / d;
+  const uint32_t x = (b - q * d) * WIDTH + uint32_t(t);
   const uint32_t y = x / d;
-  row = int(q * WIDTH + y);
+  row = int(min(q * WIDTH + y, 0x7FFFFFFFu));
   place = int(x - y * d);
 }
 
@@ -245,8 +253,8 @@ struct PermuteArgs {
 template <int ELEM, bool WIDE>
 __device__ __forceinline__ void permute_body(const PermuteArgs& p) {
   typedef typename std::conditional<WIDE, uint4, typename std::conditional<ELEM == 2, uint16_t, uint32_t>::type>::type V;
-  if (int(blockIdx.x) >= p.main_blocks) {
-    each_padding_row(p.row_slot, p.M, (long long)(blockIdx.x - p.main_blocks) * 4 + (threadIdx.x >> 6),
+  if (int(block_index()) >= p.main_blocks) {
+    each_padding_row(p.row_slot, p.M, (long long)(block_index() - p.main_blocks) * 4 + (threadIdx.x >> 6),
                      [&](long long r) { zero_row_elems(p.Y, size_t(r), p.H, ELEM); });
     return;
   }
@@ -328,8 +336,8 @@ template <bool IN_BF16, bool POW2>
 __device__ __forceinline__ void permute_fp8_body(const PermuteArgs& p) {
   const int lane = threadIdx.x & 63;
   uint8_t* Q = static_cast<uint8_t*>(p.Y);
-  if (int(blockIdx.x) >= p.main_blocks) {
-    each_padding_row(p.row_slot, p.M, (long long)(blockIdx.x - p.main_blocks) * 4 + (threadIdx.x >> 6),
+  if (int(block_index()) >= p.main_blocks) {
+    each_padding_row(p.row_slot, p.M, (long long)(block_index() - p.main_blocks) * 4 + (threadIdx.x >> 6),
                      [&](long long r) {
                        uint4* row = reinterpret_cast<uint4*>(Q + size_t(r) * p.H);
                        for (int c = lane; c < p.H / 16; c += 64) row[c] = uint4{0u, 0u, 0u, 0u};
@@ -474,12 +482,12 @@ template <bool BF16, int V>
 __device__ __forceinline__ void combine_bwd_body(const CombineBwdArgs& p) {
   constexpr int J = 4;
   __shared__ float part[4][J];
-  if (int(blockIdx.x) >= p.T) {
-    each_padding_row(p.row_slot, p.M, (long long)(blockIdx.x - p.T) * 4 + (threadIdx.x >> 6),
+  const int t = block_index();
+  if (t >= p.T) {
+    each_padding_row(p.row_slot, p.M, (long long)(t - p.T) * 4 + (threadIdx.x >> 6),
                      [&](long long r) { zero_row_elems(p.dY, size_t(r), p.H, BF16 ? 2 : 4); });
     return;
   }
-  const int t = blockIdx.x;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   for (int j0 = 0; j0 < p.k; j0 += J) {
     int row[J];

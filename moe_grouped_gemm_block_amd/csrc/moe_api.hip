@@ -61,13 +61,16 @@ bool bad(const void* p, uintptr_t a) { return p == nullptr || !aligned(p, a); }
 bool valid_type(int t) { return t == DG_IN_F32 || t == DG_IN_BF16; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+constexpr int64_t kGridX = int64_t(1) << dg::kGridBits;   // workgroups of a grid's row
+
 template <typename Args>
 int launch(void (*kernel)(Args), Args& a, int64_t blocks, int threads, hipStream_t stream) {
   if (blocks <= 0) return DG_OK;
   if (blocks > INT32_MAX) return DG_ERR_UNSUPPORTED;
   void* kargs[] = {&a};
-  const hipError_t err = hipLaunchKernel(reinterpret_cast<const void*>(kernel), dim3(unsigned(blocks)),
-                                         dim3(unsigned(threads)), kargs, 0, stream);
+  const dim3 grid(unsigned(std::min(blocks, kGridX)), unsigned(ceil_div(blocks, kGridX)));
+  const hipError_t err =
+      hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, dim3(unsigned(threads)), kargs, 0, stream);
   return err == hipSuccess ? DG_OK : DG_ERR_LAUNCH;
 }
 
@@ -263,9 +266,11 @@ int dg_grouped_wgrad_fp8(const void* dY, const void* X, const float* sX, const i
   const int64_t tiles = int64_t(a.n_tiles) * a.k_tiles;
   // (fewer tiles would leave XCDs without work: the last eighth may be short)
   a.per_xcd = tiles >= 64 ? int(ceil_div(tiles, 8)) : 0;
+  const int64_t blocks = num_groups * (a.per_xcd ? 8 * int64_t(a.per_xcd) : tiles);
+  if (blocks > kGridX) return DG_ERR_UNSUPPORTED;   // one row of a grid
   return launch(big ? (bf16 ? dg::dg_wgrad256_bf16 : dg::dg_wgrad256_f32)
                     : (bf16 ? dg::dg_wgrad128_bf16 : dg::dg_wgrad128_f32),
-                a, num_groups * (a.per_xcd ? 8 * int64_t(a.per_xcd) : tiles), 256, stream);
+                a, blocks, 256, stream);
 }
 
 }  // extern "C"

@@ -194,7 +194,7 @@ __device__ __forceinline__ void decode4(uint32_t w, float s, float* v) {
 // A thread takes 8 columns: 8 codes of g and of u and 8 values of dA in, 8
 // values of dg and of du out.  FP32 throughout, one rounding to the output type.
 // dA and dH past the caches (non-temporal), the codes' pieces of 8 bytes not: 9216
-// rows of 2 x 4096 in BF16 45.4 us, 6.7 TB/s (all plain 52.7, all non-temporal
+// rows of 2 x 4096 in BF16 45.9 us, 6.6 TB/s (all plain 52.7, all non-temporal
 // 47.4).
 template <bool BF16>
 __device__ __forceinline__ void swiglu_bwd_body(const SwigluBwdArgs& p) {

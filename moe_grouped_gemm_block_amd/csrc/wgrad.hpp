@@ -31,10 +31,11 @@
 // experts with 16384 rows unevenly, N = K = 2048, BF16: 250 us at 2.25 GHz, most
 // tiles having two to eight steps: the first loads and the stores of a tile,
 // covered by one other workgroup only.  What was slower: 128 x 128 tiles, plain
-// LDS reads and one stage 967 and 627 us; one workgroup of 256 x 256 tiles per CU
-// 360 and 329; 512 workgroups that go through shares of the tiles, loading the next
-// one before the stores of the last, 329 and 304 (where rows are even, 134 instead
-// of 151 us for 256 each); the experts in order of their rows, the same on average.
+// LDS reads and one stage 967 and 627 us; one workgroup of 256 x 256 tiles per CU,
+// with a third less LDS traffic, 340 and 303; 512 workgroups that go through
+// shares of the tiles, loading the next one before the stores of the last, 329 and
+// 304 (where rows are even, 134 instead of 151 us for 256 each); the experts in
+// order of their rows, the same on average.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -142,7 +143,7 @@ __device__ __forceinline__ void wgrad_body(const WgradArgs& p) {
   expert_rows(p, e, r0, r1);
   r0 = __builtin_amdgcn_readfirstlane(r0);
   r1 = __builtin_amdgcn_readfirstlane(r1);
-  const int steps = (r1 - r0 + BR - 1) / BR;
+  const int full = (r1 - r0) / BR, last = (r1 - r0) % BR, steps = full + (last > 0);
   const int N = p.N, K = p.K, Kb = p.Kb;
   const uint32_t lds0 = uint32_t(reinterpret_cast<uintptr_t>((lds_u8*)lds));
 
@@ -150,7 +151,6 @@ __device__ __forceinline__ void wgrad_body(const WgradArgs& p) {
   // last row: rows past the expert's read zeros.  All but the last steps have BR
   // rows.  (In scalar registers; as a function of s alone it would go through the
   // vector units.)
-  const int full = (r1 - r0) / BR, last = (r1 - r0) % BR;
   struct Sizes {
     uint32_t full, last;
   };

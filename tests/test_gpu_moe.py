@@ -225,6 +225,72 @@ def test_rows_past_32_bit_offsets():
     assert np.array_equal(q[rows[:, 1]].cpu().numpy(), codes) and np.array_equal(s[rows[:, 1]].cpu().numpy(), scales)
 
 
+def test_grids_past_32_bit_work_items():
+    """A thread per element of an odd width, a workgroup per token, eight threads
+    per block: more work-items than one dimension of a grid has (2^32, or the 2^31
+    from which workgroups are laid out in two)."""
+    T, H = 1048577, 4099
+    assert T * H > 1 << 32
+    y = torch.randn(5, H, device=DEV).bfloat16()
+    slot = (torch.arange(T, device=DEV, dtype=torch.int32) % 5)[:, None].contiguous()
+    out = dg.moe_combine(y, slot)
+    for t in range(0, T, 1 << 17):
+        assert torch.equal(out[t:t + (1 << 17)], y[slot[t:t + (1 << 17), 0].long()])
+    at = [0, 1, (1 << 31) // H + 1, T - 2, T - 1]
+    slot.fill_(-1)
+    slot[at, 0] = torch.tensor([4, 0, 3, 1, 6], device=DEV, dtype=torch.int32)
+    row_slot = torch.tensor([at[1], at[3], -1, at[2], at[0], -1, at[4]], device=DEV, dtype=torch.int32)
+    got = dg.moe_permute(out, slot, row_slot)
+    for r, t in enumerate(row_slot.tolist()):
+        assert torch.equal(got[r], out[t]) if t >= 0 else not got[r].any()
+    del out, got
+
+    T, H = (1 << 24) + 3, 8
+    at = [0, 1 << 23, T - 1]
+    d = torch.randn(T, H, device=DEV)
+    y = torch.randn(4, H, device=DEV)
+    slot = torch.full((T, 1), -1, device=DEV, dtype=torch.int32)
+    slot[at, 0] = torch.tensor([2, 0, 1], device=DEV, dtype=torch.int32)
+    row_slot = torch.tensor([at[1], at[2], at[0], -1], device=DEV, dtype=torch.int32)
+    dy, dw = dg.moe_combine_bwd(d, y, slot, row_slot, torch.ones(T, 1, device=DEV))
+    assert torch.equal(dy[:3], d[row_slot[:3].long()]) and not dy[3].any()
+    assert torch.count_nonzero(dw) == 3
+    want = (d[at].double() * y[slot[at, 0].long()].double())
+    assert bool(((dw[at, 0].double() - want.sum(1)).abs() <= 18 * 2.0 ** -24 * want.abs().sum(1)).all())
+    del d, dw
+
+    T, H = (1 << 28) + 3, 16
+    at = [0, 1 << 27, T - 1]
+    x = torch.zeros(T, H, device=DEV, dtype=torch.bfloat16)
+    x[at] = torch.randn(3, H, device=DEV).bfloat16()
+    slot = torch.full((T, 1), -1, device=DEV, dtype=torch.int32)
+    slot[at, 0] = torch.arange(3, device=DEV, dtype=torch.int32)
+    row_slot = torch.tensor(at + [-1], device=DEV, dtype=torch.int32)
+    q, s = dg.moe_permute_fp8(x, slot, row_slot)
+    codes, scales = O.quantise(x[at].double().cpu().numpy(), True)
+    assert np.array_equal(q[:3].cpu().numpy(), codes) and np.array_equal(s[:3].cpu().numpy(), scales)
+    assert not q[3].any() and float(s[3]) == 1
+    del slot
+    h = x.new_zeros(T, 2 * H)
+    h[at] = torch.randn(3, 2 * H, device=DEV).bfloat16()
+    for got, want in zip(dg.swiglu_fp8(h), dg.swiglu_fp8(h[at])):
+        assert torch.equal(got[at], want)
+
+
+def test_plan_of_most_rows():
+    """As many rows as are counted in 32 bits: the rest of them is padding."""
+    M = (1 << 31) - 1
+    for T in (3, 4097):                                          # one workgroup, several
+        ids = make_ids(T, 2, 4, seed=3)
+        plan = dg.moe_sort(dev(ids.astype(np.int32)), 4, align=1, rows=M)
+        short = dg.moe_sort(dev(ids.astype(np.int32)), 4, align=1)
+        n = short.row_slot.numel()
+        assert torch.equal(plan.slot_row, short.slot_row) and torch.equal(plan.row_slot[:n], short.row_slot)
+        assert int(plan.row_slot[n:].max()) == -1 and int(plan.row_slot[n:].min()) == -1
+        assert int(plan.group_offsets[-1]) == M
+        del plan
+
+
 def test_another_stream_and_poisoned_memory():
     """Calls on a stream of their own, with inputs written there just before."""
     _, M, ref, _ = plan_for(257, 4, 16, 128, seed=1)

@@ -114,6 +114,12 @@ def test_wgrad_validation(kw, want):
     assert call(dg.dg_grouped_wgrad_fp8, base, kw) == want
 
 
+@pytest.mark.parametrize("kw", [dict(G=(1 << 23) + 1, N=8, K=16), dict(G=1 << 15, N=4096, K=4096)])
+def test_wgrad_grid_limit(kw):
+    base = dict(dY=P, X=P, sX=P, offs=P, counts=P, G=4, M=512, N=256, K=256, dW=P, out=0, acc=0)
+    assert call(dg.dg_grouped_wgrad_fp8, base, kw) == UNSUP
+
+
 def test_helpers_refuse_host_tensors_and_wrong_types():
     f, i = torch.zeros(4, 32), torch.zeros(4, 2, dtype=torch.int32)
     with pytest.raises(TypeError):
