@@ -227,13 +227,14 @@ __device__ __forceinline__ void zero_row_elems(void* Y, size_t row, int H, int e
 // Row and place of item (block_index() WIDTH + t) where a row has `per` items (per
 // WIDTH below 2^31, t < WIDTH): two divisions in 32 bits; the one in 64 bits that
 // this stands for takes over a hundred instructions, a fifth of the gated
-// activation's.  Past 2^31 - 1, behind every row, the row stays there.
+// activation's.  Unsigned: the last workgroups' rows may lie past 2^31, behind the
+// matrix.
 template <int WIDTH>
-__device__ __forceinline__ void row_and_place(int t, int per, int& row, int& place) {
+__device__ __forceinline__ void row_and_place(int t, int per, uint32_t& row, int& place) {
   const uint32_t d = uint32_t(per), b = block_index(), q = b / d;
   const uint32_t x = (b - q * d) * WIDTH + uint32_t(t);
   const uint32_t y = x / d;
-  row = int(min(q * WIDTH + y, 0x7FFFFFFFu));
+  row = q * WIDTH + y;
   place = int(x - y * d);
 }
 
@@ -259,9 +260,10 @@ __device__ __forceinline__ void permute_body(const PermuteArgs& p) {
     return;
   }
   const int per = WIDE ? p.H * ELEM / 16 : p.H;               // pieces of a row
-  int t, c;
+  uint32_t t;
+  int c;
   row_and_place<256>(threadIdx.x, per, t, c);
-  if (t >= p.T) return;
+  if (t >= uint32_t(p.T)) return;
   const V v = static_cast<const V*>(p.X)[size_t(t) * per + c];
   for (int j = 0; j < p.k; ++j) {
     const int row = p.slot_row[(long long)t * p.k + j];
@@ -345,16 +347,17 @@ __device__ __forceinline__ void permute_fp8_body(const PermuteArgs& p) {
                      });
     return;
   }
-  int t, kb;
+  uint32_t t;
+  int kb;
   row_and_place<32>(threadIdx.x >> 3, p.Kb, t, kb);
   const int col = kb * 128 + 16 * (lane & 7);
-  const bool in = t < p.T && col < p.H;
+  const bool in = t < uint32_t(p.T) && col < p.H;
   Q1Buf<IN_BF16> b;
   load_q16(b, p.X, in ? size_t(t) * p.H + col : 0, in);
   // the first rows are looked up while X is on its way
   constexpr int J = 8;
   int rows[J];
-  const int32_t* slot_row = p.slot_row + (t < p.T ? (long long)t * p.k : 0);
+  const int32_t* slot_row = p.slot_row + (t < uint32_t(p.T) ? (long long)t * p.k : 0);
 #pragma unroll
   for (int j = 0; j < J; ++j) rows[j] = in && j < p.k ? slot_row[j] : -1;
   float amax = 0.f;
@@ -377,9 +380,10 @@ __device__ __forceinline__ void permute_fp8_body(const PermuteArgs& p) {
   }
   // scales in whole lines: the workgroup's 32 blocks of each choice side by side
   __syncthreads();
-  int t2, kb2;
+  uint32_t t2;
+  int kb2;
   row_and_place<32>(threadIdx.x & 31, p.Kb, t2, kb2);
-  if (t2 >= p.T) return;
+  if (t2 >= uint32_t(p.T)) return;
   for (int j = threadIdx.x >> 5; j < p.k; j += 8) {
     const int row = p.slot_row[(long long)t2 * p.k + j];
     if (row >= 0 && row < p.M) p.S[size_t(row) * p.Kb + kb2] = scale[threadIdx.x & 31];
@@ -443,9 +447,10 @@ __device__ __forceinline__ void store_values(void* dst, size_t e0, const float* 
 // choices, in FP32, rounded once.  Rows of dropped slots are not read.
 template <bool BF16, int V>
 __device__ __forceinline__ void combine_body(const CombineArgs& p) {
-  int t, c;
+  uint32_t t;
+  int c;
   row_and_place<256>(threadIdx.x, p.H / V, t, c);
-  if (t >= p.T) return;
+  if (t >= uint32_t(p.T)) return;
   c *= V;
   float acc[V];
 #pragma unroll

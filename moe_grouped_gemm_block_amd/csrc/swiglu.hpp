@@ -79,10 +79,11 @@ __device__ __forceinline__ uint32_t e4m3_of_f64(double v) {
 template <bool IN_BF16, bool CHECKPOINT>
 __device__ __forceinline__ void swiglu_body(const SwigluArgs& p) {
   const int lane = threadIdx.x & 63;
-  int m, ib;
+  uint32_t m;
+  int ib;
   row_and_place<32>(threadIdx.x >> 3, p.Ib, m, ib);
   const int col = ib * 128 + 16 * (lane & 7);
-  const bool in = m < p.M && col < p.I;
+  const bool in = m < uint32_t(p.M) && col < p.I;
   Q1Buf<IN_BF16> bg, bu;
   const size_t e0 = in ? size_t(m) * 2 * p.I + col : 0;
   load_q16(bg, p.H, e0, in);
@@ -115,7 +116,7 @@ __device__ __forceinline__ void swiglu_body(const SwigluArgs& p) {
       store16<false>(p.Hq + e0, u32x4_nt{cg.w[0], cg.w[1], cg.w[2], cg.w[3]});
       store16<false>(p.Hq + e0 + p.I, u32x4_nt{cu.w[0], cu.w[1], cu.w[2], cu.w[3]});
     }
-    if (m < p.M && (lane & 7) == 0) {
+    if (m < uint32_t(p.M) && (lane & 7) == 0) {
       p.sH[(size_t(m) * 2) * p.Ib + ib] = sg;
       p.sH[(size_t(m) * 2 + 1) * p.Ib + ib] = su;
     }
@@ -169,7 +170,7 @@ __device__ __forceinline__ void swiglu_body(const SwigluArgs& p) {
     }
   }
   if (in) store16<false>(p.A + size_t(m) * p.I + col, u32x4_nt{w[0], w[1], w[2], w[3]});
-  if (m < p.M && (lane & 7) == 0) p.sA[size_t(m) * p.Ib + ib] = s;
+  if (m < uint32_t(p.M) && (lane & 7) == 0) p.sA[size_t(m) * p.Ib + ib] = s;
 }
 
 struct SwigluBwdArgs {
@@ -194,13 +195,14 @@ __device__ __forceinline__ void decode4(uint32_t w, float s, float* v) {
 // A thread takes 8 columns: 8 codes of g and of u and 8 values of dA in, 8
 // values of dg and of du out.  FP32 throughout, one rounding to the output type.
 // dA and dH past the caches (non-temporal), the codes' pieces of 8 bytes not: 9216
-// rows of 2 x 4096 in BF16 45.9 us, 6.6 TB/s (all plain 52.7, all non-temporal
+// rows of 2 x 4096 in BF16 45.5 us, 6.7 TB/s (all plain 52.7, all non-temporal
 // 47.4).
 template <bool BF16>
 __device__ __forceinline__ void swiglu_bwd_body(const SwigluBwdArgs& p) {
-  int m, col;
+  uint32_t m;
+  int col;
   row_and_place<256>(threadIdx.x, p.I / 8, m, col);
-  if (m >= p.M) return;
+  if (m >= uint32_t(p.M)) return;
   col *= 8;
   const size_t h0 = size_t(m) * 2 * p.I + col;
   const uint2 wg = *reinterpret_cast<const uint2*>(p.Hq + h0);
