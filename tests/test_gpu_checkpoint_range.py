@@ -1,0 +1,95 @@
+"""The gated activation's gradient over the whole range of what a checkpoint can
+hold.  Checkpoints are made directly, as codes and scales.  Needs a GPU.
+
+Tolerance.  The factors' relative errors are as in test_gpu_checkpoint.py: 2^-20
+of the magnitudes of the terms, and half a step (2^-8) for a BF16 result.  The
+only absolute term is FP32's smallest step, 2^-149, for an FP32 result and the
+smallest normal number, 2^-126, for a BF16 one."""
+import sys
+
+import numpy as np
+import pytest
+import torch
+
+from moe_grouped_gemm_block_amd import dg
+from oracle import moe as O
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+DTYPE = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def log(*a):
+    print(*a, file=sys.stderr, flush=True)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    dg.lib()
+
+
+def checkpoint(g, u):
+    """(codes, scales) of [M][I] gates and factors, exactly as the oracle quantises."""
+    (qg, sg), (qu, su) = O.quantise(g, True), O.quantise(u, True)
+    return np.concatenate([qg, qu], 1), np.stack([sg, su], 1)
+
+
+def run(da, Hq, sH, dtype):
+    """(dg, du) of the kernel and dA as it saw it, in float64."""
+    d = torch.from_numpy(np.ascontiguousarray(da)).to(DTYPE[dtype]).to(DEV)
+    dH = dg.swiglu_fp8_bwd(d, torch.from_numpy(Hq).to(DEV), torch.from_numpy(np.ascontiguousarray(sH)).to(DEV))
+    torch.cuda.synchronize()
+    I = da.shape[1]
+    got = dH.double().cpu().numpy()
+    return got[:, :I], got[:, I:], d.double().cpu().numpy()
+
+
+def decoded(Hq, sH, I):
+    return (O.dequantise(Hq[:, i * I:(i + 1) * I], np.ascontiguousarray(sH[:, i])) for i in (0, 1))
+
+
+def check(da, Hq, sH, dtype):
+    I = da.shape[1]
+    got_g, got_u, d = run(da, Hq, sH, dtype)
+    g, u = decoded(Hq, sH, I)
+    with np.errstate(over="ignore"):
+        want_g, want_u, mass = O.swiglu_bwd(d, g, u)
+    half = 2.0 ** -8 if dtype == "bf16" else 0.0
+    least = 2.0 ** -126 if dtype == "bf16" else 2.0 ** -149
+    top = float(torch.finfo(DTYPE[dtype]).max)
+    for name, got, want, m in (("dg", got_g, want_g, mass), ("du", got_u, want_u, np.abs(want_u))):
+        bound = half * np.abs(want) + 2.0 ** -20 * m + least
+        ok = np.abs(got - want) <= bound
+        ok |= (np.abs(want) + bound > top) & np.isinf(got) & (np.sign(got) == np.sign(want))
+        bad = np.argwhere(~ok)
+        assert not len(bad), [(name, i.tolist(), float(g[tuple(i)]), float(u[tuple(i)]), float(got[tuple(i)]),
+                               float(want[tuple(i)])) for i in bad[:4]]
+
+
+FAR = (-3.3e38, -1e36, -1e33, -1e30, -1e20, -1e6, -1000.0, -300.0, -150.0, -120.0, -104.0, -100.0, -96.0, -90.0,
+       -88.0, -87.0, -81.0, -80.0, -72.0, -64.0, -60.0, -57.0, -56.0, -52.0, -40.0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("size", [1.0, 2.0 ** 40, 2.0 ** 90])
+def test_far_negative_gates(dtype, size):
+    """The gradient goes to 0 with the gate, as e^g does: 0 at the far end, and
+    right relative to itself where a large u brings it back into range."""
+    log(f"far negative gates {dtype} size={size:g}")
+    rng = np.random.default_rng(1)
+    g = np.repeat(np.array(FAR)[:, None], 144, 1)              # a whole block and a partial one
+    u = rng.standard_normal(g.shape) * size
+    check(rng.standard_normal(g.shape), *checkpoint(g, u), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_far_gates_beside_ordinary_ones(dtype):
+    """Within one block, and with positive gates as far out."""
+    rng = np.random.default_rng(2)
+    g = rng.standard_normal((64, 272)) * np.exp2(rng.uniform(-2, 9, (64, 1)))
+    g[::5, 3] = 448 * 2.0 ** 119
+    g[1::5, 7] = -3.35e38                                      # its code rounds up to 2^128
+    u = rng.standard_normal(g.shape)
+    check(rng.standard_normal(g.shape), *checkpoint(g, u), dtype)
