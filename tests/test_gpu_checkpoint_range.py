@@ -1,5 +1,6 @@
 """The gated activation's gradient over the whole range of what a checkpoint can
-hold.  Checkpoints are made directly, as codes and scales.  Needs a GPU.
+hold: gates far out on both sides, and NaN.  Checkpoints are made
+directly, as codes and scales.  Needs a GPU.
 
 Tolerance.  The factors' relative errors are as in test_gpu_checkpoint.py: 2^-20
 of the magnitudes of the terms, and half a step (2^-8) for a BF16 result.  The
@@ -18,6 +19,7 @@ pytestmark = pytest.mark.gpu
 
 DEV = "cuda:0"
 DTYPE = {"bf16": torch.bfloat16, "f32": torch.float32}
+NAN_CODE = 0x7F
 
 
 def log(*a):
@@ -93,3 +95,33 @@ def test_far_gates_beside_ordinary_ones(dtype):
     g[1::5, 7] = -3.35e38                                      # its code rounds up to 2^128
     u = rng.standard_normal(g.shape)
     check(rng.standard_normal(g.shape), *checkpoint(g, u), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("where", ["gate code", "factor code", "gate scale", "factor scale"])
+@pytest.mark.parametrize("scale", [2.0 ** -9, 1.0])
+def test_nan_reaches_the_gradient(dtype, where, scale):
+    """A NaN in the checkpoint is a NaN in what depends on it, and nowhere else."""
+    I = 256
+    rng = np.random.default_rng(3)
+    Hq, sH = checkpoint(rng.standard_normal((3, I)) * 300 * scale, rng.standard_normal((3, I)) * 300 * scale)
+    da = rng.standard_normal((3, I))
+    clean = run(da, Hq, sH, dtype)
+    if where == "gate code":
+        Hq[1, 5] = NAN_CODE
+        hit_g, hit_u = (slice(5, 6),) * 2
+    elif where == "factor code":
+        Hq[1, I + 5] = NAN_CODE | 0x80
+        hit_g, hit_u = slice(5, 6), slice(0, 0)
+    elif where == "gate scale":
+        sH[1, 0, 1] = np.nan
+        hit_g, hit_u = (slice(128, 256),) * 2
+    else:
+        sH[1, 1, 1] = np.nan
+        hit_g, hit_u = slice(128, 256), slice(0, 0)
+    got = run(da, Hq, sH, dtype)
+    for c, v, hit in ((clean[0], got[0], hit_g), (clean[1], got[1], hit_u)):
+        want = np.zeros(v.shape, bool)
+        want[1, hit] = True
+        assert np.array_equal(np.isnan(v), want), where
+        assert np.array_equal(v[~want], c[~want]), where
