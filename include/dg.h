@@ -441,7 +441,8 @@ int dg_swiglu_fp8(const void* H, int in_dtype, void* A, float* sA, void* Hq, flo
  * Its gradient from the checkpoint: with g, u decoded from Hq, sH and p =
  * 1 / (1 + exp(-g)), dH[:, :I] = dA u p (1 + g (1 - p)) and dH[:, I:] = dA g p.
  * dA [M][I] and dH [M][2 I] are of `dtype`.  I a multiple of 16.  The gradient is
- * that of the real numbers g and u at any gate, 0 far below 0.  A NaN code or
+ * that of the real numbers g and u at any gate, 0 far below 0, and infinite only
+ * where it exceeds `dtype` itself, not a product on the way.  A NaN code or
  * scale gives NaN in what depends on it: dg and du for g's, dg for u's.
  */
 int dg_swiglu_fp8_bwd(const void* dA, int dtype, const void* Hq, const float* sH, void* dH, int64_t M,

@@ -240,12 +240,15 @@ __device__ __forceinline__ void swiglu_bwd_body(const SwigluBwdArgs& p) {
     const float pr = __builtin_amdgcn_rcpf(1.f + e);
     const float x = g[v] * pr;
     du[v] = d[v] * x;
-    dg_[v] = d[v] * u[v] * __builtin_fmaf(x, e * pr, pr);
+    dg_[v] = d[v] * (u[v] * __builtin_fmaf(x, e * pr, pr));
   }
-  // (the largest numbers' codes may round up past FP32's end: infinite gates, and
-  // factors of scales above 2^100, are in double too)
-  const bool large = !(su <= 0x1p100f);
-  bool far = large;
+  // Blocks with smaller or larger scales are in double as a whole: with these, g p
+  // and u (p + g p (1 - p)) are normal numbers before dA comes to them (gates of
+  // at least -56: p >= 2^-81 and u >= 2^-49; where p is near 1/2, g >= 2^-109), so
+  // that only the results themselves can leave FP32's range.  Gates whose codes
+  // round up past its end are infinite here, and far.
+  const bool g_out = !(sg >= 0x1p-100f), u_out = !(su >= 0x1p-40f && su <= 0x1p100f);
+  bool far = g_out || u_out;
   if (__builtin_expect(!(sg <= 0.125f), 0)) {
 #pragma unroll
     for (int v = 0; v < 8; ++v) far |= !(g[v] >= -56.f && g[v] <= __FLT_MAX__);
@@ -260,8 +263,8 @@ __device__ __forceinline__ void swiglu_bwd_body(const SwigluBwdArgs& p) {
 #pragma unroll 1
     for (int i = 0; i < 8; ++i) {
       const double gd = double(code_value(wg, i)) * double(sg);
-      const bool ordinary = gd >= -56.0 && gd <= __FLT_MAX__;
-      if (ordinary && !large) continue;
+      const bool ordinary = gd >= -56.0 && gd <= __FLT_MAX__ && !g_out;
+      if (ordinary && !u_out) continue;
       float di, a, b;
       load_values<BF16, 1>(p.dA, size_t(m) * p.I + col + i, &di);
       silu_mul_bwd_f64(di, gd, double(code_value(wu, i)) * double(su), a, b);

@@ -1,6 +1,7 @@
 """The gated activation's gradient over the whole range of what a checkpoint can
-hold: gates far out on both sides, and NaN.  Checkpoints are made
-directly, as codes and scales.  Needs a GPU.
+hold: gates far out on both sides, NaN, and products that leave FP32's range on
+the way to a result inside it.  Checkpoints are made directly, as codes and
+scales.  Needs a GPU.
 
 Tolerance.  The factors' relative errors are as in test_gpu_checkpoint.py: 2^-20
 of the magnitudes of the terms, and half a step (2^-8) for a BF16 result.  The
@@ -125,3 +126,32 @@ def test_nan_reaches_the_gradient(dtype, where, scale):
         want[1, hit] = True
         assert np.array_equal(np.isnan(v), want), where
         assert np.array_equal(v[~want], c[~want]), where
+
+
+# gate, factor and incoming gradient: the result is in range, a product on the way is not
+PRODUCTS = [(-56.0, 1e25, 1e20), (-60.0, 1e25, 1e20), (-40.0, 1e30, 1e15), (1.0, 1e-30, 1e30), (1.0, 1e30, 1e-30),
+            (-52.0, 1e-30, 1e38), (3.0, 3.0e38, 1e-3), (44.0, 3.0e38, 1e-20), (1e-38, 1.0, 1e38), (1e-35, 1e-5, 1e30),
+            (1e-30, 1e-30, 1e30), (3e38, 2.0, 1e-3), (3e38, 1e-38, 1e-3), (-80.0, 1e38, 1e30), (20.0, 1e-38, 1e38),
+            (-56.0, 2.0 ** -40, 1e38), (-56.0, 2.0 ** 100, 1.0), (2.0 ** -50, 1.0, 1e38)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_products_that_leave_the_range_on_the_way(dtype):
+    rng = np.random.default_rng(4)
+    rows = np.array(PRODUCTS)
+    wobble = lambda: 1 + rng.uniform(0, 0.1, (len(rows), 144))
+    g, u, da = (rows[:, i:i + 1] * wobble() for i in range(3))
+    top = 3.38e38                                              # dA itself is finite
+    check(np.clip(da, -top, top), *checkpoint(np.clip(g, -top, top), np.clip(u, -top, top)), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_random_exponents(dtype):
+    """Gates, factors and gradients of any size against each other."""
+    rng = np.random.default_rng(5)
+    M, I = 256, 144
+    size = lambda lo, hi: np.exp2(rng.uniform(lo, hi, (M, 1)))
+    g = rng.uniform(-1, 1, (M, I)) * size(-120, 127)
+    g[::2] = rng.uniform(-1, 1, (M // 2, I)) * size(-8, 8)[::2]
+    u = rng.uniform(-1, 1, (M, I)) * size(-126, 127)
+    check(rng.uniform(-1, 1, (M, I)) * size(-100, 126), *checkpoint(g, u), dtype)
