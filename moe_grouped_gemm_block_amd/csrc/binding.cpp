@@ -126,23 +126,12 @@ Tensor output(PyObject* o, const char* name, at::IntArrayRef shape, ScalarType d
   return t;
 }
 
-// Elements of `dtype` from the `at`-th on of `whole`, as a tensor of their own.
-Tensor part(const Tensor& whole, ScalarType dtype, int64_t at, at::IntArrayRef sizes) {
-  Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(whole.storage()), whole.key_set(),
-                                                      c10::scalarTypeToTypeMeta(dtype));
+// Elements from the `at`-th on of `whole`, as a tensor of their own.
+Tensor part(const Tensor& whole, int64_t at, at::IntArrayRef sizes) {
+  Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(whole.storage()), whole.key_set(), whole.dtype());
   t.unsafeGetTensorImpl()->set_storage_offset(at);
   t.unsafeGetTensorImpl()->set_sizes_contiguous(sizes);
   return t;
-}
-
-// New codes [M][width] and behind them in the same memory, since they are used
-// together, their scales (shape `scales`): the gated activation with a checkpoint
-// takes 5.8 us a call at 256 rows of 2 x 2048, with four allocations 6.4.
-void create_codes(Tensor& Q, Tensor& S, int64_t M, int64_t width, at::IntArrayRef scales, const Tensor& like) {
-  const int64_t at = (M * width + 3) / 4;
-  const Tensor all = create({4 * (at + c10::multiply_integers(scales))}, at::kByte, like);
-  Q = part(all, at::kByte, 0, {M, width});
-  S = part(all, at::kFloat, at, scales);
 }
 
 int64_t integer(PyObject* o, const char* name) {
@@ -213,9 +202,9 @@ PyObject* moe_sort(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (M < 0 || M > INT32_MAX || ws < 0) return failure(DG_ERR_INVALID_ARG, "dg_moe_sort");
   // one allocation for the plan and the workspace: four cost 2 us more
   const Tensor all = create({2 * int64_t(G) + 1 + M + T * k + ws / 4}, at::kInt, ids);
-  const Tensor offs = part(all, at::kInt, 0, {G + 1}), counts = part(all, at::kInt, G + 1, {G});
-  const Tensor row_slot = part(all, at::kInt, 2 * int64_t(G) + 1, {M});
-  const Tensor slot_row = part(all, at::kInt, 2 * int64_t(G) + 1 + M, {T, k});
+  const Tensor offs = part(all, 0, {G + 1}), counts = part(all, G + 1, {G});
+  const Tensor row_slot = part(all, 2 * int64_t(G) + 1, {M});
+  const Tensor slot_row = part(all, 2 * int64_t(G) + 1 + M, {T, k});
   void* work = ws ? data<int32_t>(all) + 2 * int64_t(G) + 1 + M + T * k : nullptr;
   const int st = lib.moe_sort(ids.data_ptr(), ids.scalar_type() == at::kLong ? DG_IDX_I64 : DG_IDX_I32, T, int(k), G,
                               align, M, data<int32_t>(offs), data<int32_t>(counts), data<int32_t>(row_slot),
@@ -251,13 +240,8 @@ PyObject* moe_permute_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int64_t T = X.size(0), H = X.size(1);
   const int k = check_slots(slot_row, T);
   const int64_t M = check_rows(row_slot);
-  Tensor Q, S;
-  if (a[4] == Py_None && a[5] == Py_None) {
-    create_codes(Q, S, M, H, {M, (H + 127) / 128}, X);
-  } else {
-    Q = output(a[4], "Q", {M, H}, at::kByte, X);
-    S = output(a[5], "S", {M, (H + 127) / 128}, at::kFloat, X);
-  }
+  const Tensor Q = output(a[4], "Q", {M, H}, at::kByte, X);
+  const Tensor S = output(a[5], "S", {M, (H + 127) / 128}, at::kFloat, X);
   const int st = lib.moe_permute_fp8(X.data_ptr(), code, Q.data_ptr(), data<float>(S), mode, data<int32_t>(slot_row),
                                      data<int32_t>(row_slot), T, k, M, H, stream());
   if (st != DG_OK) return failure(st, "dg_moe_permute_fp8");
@@ -317,9 +301,19 @@ PyObject* swiglu_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (checkpoint < 0) return nullptr;
   if (H.size(1) % 2) value_error("H must have an even number of columns");
   const int64_t M = H.size(0), I = H.size(1) / 2, Ib = (I + 127) / 128;
-  Tensor A, sA, Hq, sH;
-  create_codes(A, sA, M, I, {M, Ib}, H);
-  if (checkpoint) create_codes(Hq, sH, M, 2 * I, {M, 2, Ib}, H);
+  const Tensor A = create({M, I}, at::kByte, H);
+  Tensor sA, Hq, sH;
+  if (checkpoint) {
+    // the scales, 1/32 of the codes' bytes, in one allocation (256 rows of 2 x 2048:
+    // 6.4 us a call, with two 6.8); codes are of another type, which could not be
+    // saved to a file together with scales in the same memory
+    const Tensor scales = create({3 * M * Ib}, at::kFloat, H);
+    sA = part(scales, 0, {M, Ib});
+    sH = part(scales, M * Ib, {M, 2, Ib});
+    Hq = create({M, 2 * I}, at::kByte, H);
+  } else {
+    sA = create({M, Ib}, at::kFloat, H);
+  }
   // an empty checkpoint's addresses are null, which would ask for none: no work either way
   const int st = lib.swiglu_fp8(H.data_ptr(), code, A.data_ptr(), data<float>(sA), checkpoint ? Hq.data_ptr() : nullptr,
                                 checkpoint ? data<float>(sH) : nullptr, M, I, stream());

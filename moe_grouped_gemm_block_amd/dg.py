@@ -489,7 +489,7 @@ def moe_permute_fp8(X, slot_row, row_slot, scale="pow2", Q=None, S=None, stream=
     """The same, quantised: E4M3 codes Q[M][H] and one FP32 scale per row and 128
     columns, S[M][ceil(H/128)] (A and sA of the grouped products).  scale:
     "pow2" (powers of two: what grouped_wgrad_fp8 reads without rounding) or
-    "amax" (amax / 448).  New Q and S share an allocation."""
+    "amax" (amax / 448)."""
     return _call("moe_permute_fp8", stream, X, slot_row, row_slot, scale_code(scale), Q, S)
 
 
@@ -509,8 +509,7 @@ def swiglu_fp8(H, checkpoint=True, stream=None):
     """a = u g / (1 + exp(-g)) of H[M][2 I] = [g | u] (bfloat16 or float32) in 8
     bits: (A[M][I], sA[M][ceil(I/128)], Hq[M][2 I], sH[M][2][ceil(I/128)]), E4M3
     codes with power-of-two scales.  Hq, sH are H's checkpoint for
-    swiglu_fp8_bwd; None without `checkpoint`.  Codes and their scales share an
-    allocation."""
+    swiglu_fp8_bwd; None without `checkpoint`.  sA and sH share an allocation."""
     return _call("swiglu_fp8", stream, H, checkpoint)
 
 
