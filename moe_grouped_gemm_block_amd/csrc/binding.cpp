@@ -200,15 +200,16 @@ PyObject* moe_sort(PyObject*, PyObject* const* a, Py_ssize_t n) {
   int64_t M = k > INT32_MAX ? -1 : lib.moe_rows(T, int(k), G, align);
   if (a[3] != Py_None && M >= 0) M = integer(a[3], "rows");
   if (M < 0 || M > INT32_MAX || ws < 0) return failure(DG_ERR_INVALID_ARG, "dg_moe_sort");
-  // one allocation for the plan and the workspace: four cost 2 us more
-  const Tensor all = create({2 * int64_t(G) + 1 + M + T * k + ws / 4}, at::kInt, ids);
+  // one allocation for the plan: four cost 2 us more
+  const Tensor all = create({2 * int64_t(G) + 1 + M + T * k}, at::kInt, ids);
   const Tensor offs = part(all, 0, {G + 1}), counts = part(all, G + 1, {G});
   const Tensor row_slot = part(all, 2 * int64_t(G) + 1, {M});
   const Tensor slot_row = part(all, 2 * int64_t(G) + 1 + M, {T, k});
-  void* work = ws ? data<int32_t>(all) + 2 * int64_t(G) + 1 + M + T * k : nullptr;
+  // (the workspace is free for the stream's later work when the call returns)
+  const Tensor work = ws ? create({ws}, at::kByte, ids) : Tensor();
   const int st = lib.moe_sort(ids.data_ptr(), ids.scalar_type() == at::kLong ? DG_IDX_I64 : DG_IDX_I32, T, int(k), G,
                               align, M, data<int32_t>(offs), data<int32_t>(counts), data<int32_t>(row_slot),
-                              data<int32_t>(slot_row), work, stream());
+                              data<int32_t>(slot_row), ws ? work.data_ptr() : nullptr, stream());
   if (st != DG_OK) return failure(st, "dg_moe_sort");
   return tuple(offs, counts, row_slot, slot_row);
   END_HANDLE_TH_ERRORS

@@ -38,3 +38,12 @@ def test_codes_and_scales_are_saved_and_loaded(M, I):
         for codes in outputs[::2]:
             assert codes.untyped_storage().nbytes() == codes.numel()      # nothing beside them
     assert all(torch.equal(a, b) for a, b in zip(plan, saved_and_loaded(tuple(plan))))
+
+
+@pytest.mark.parametrize("T,k,G", [(100, 2, 64), (10000, 4, 256)])
+def test_a_plan_keeps_no_workspace(T, k, G):
+    """The sort of more than 8192 slots has a workspace, which ends with the call."""
+    plan = dg.moe_sort(torch.randint(0, G, (T, k), device=DEV), G)
+    assert (dg.dg_moe_sort_workspace(T, k, G) > 0) == (T * k > 8192)
+    held = {t.untyped_storage().data_ptr(): t.untyped_storage().nbytes() for t in plan}
+    assert sum(held.values()) == sum(4 * t.numel() for t in plan)
