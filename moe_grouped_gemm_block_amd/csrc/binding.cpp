@@ -118,11 +118,13 @@ Tensor create(at::IntArrayRef shape, ScalarType dtype, const Tensor& like) {
   return at::detail::empty_cuda(shape, dtype, like.device(), c10::nullopt);
 }
 
-// The output `o`, checked, or a new tensor.
+// The output `o`, checked, or a new tensor.  What is written counts as written:
+// autograd then sees a saved tensor that has changed.
 Tensor output(PyObject* o, const char* name, at::IntArrayRef shape, ScalarType dtype, const Tensor& like) {
   if (o == nullptr || o == Py_None) return create(shape, dtype, like);
   const Tensor& t = tensor(o, name);
   check(t, name, {dtype}, shape);
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
   return t;
 }
 

@@ -47,3 +47,42 @@ def test_a_plan_keeps_no_workspace(T, k, G):
     assert (dg.dg_moe_sort_workspace(T, k, G) > 0) == (T * k > 8192)
     held = {t.untyped_storage().data_ptr(): t.untyped_storage().nbytes() for t in plan}
     assert sum(held.values()) == sum(4 * t.numel() for t in plan)
+
+
+def test_written_outputs_change_their_version():
+    """A tensor that an operator writes counts as written: autograd refuses to
+    use it where an earlier operation saved what it held."""
+    T, k, G, H = 40, 2, 4, 128
+    x = torch.randn(T, H, device=DEV).bfloat16()
+    plan = dg.moe_sort(torch.randint(0, G, (T, k), device=DEV), G)
+    M = plan.row_slot.numel()
+    w = torch.rand(T, k, device=DEV)
+    new = lambda *shape, dtype=torch.bfloat16: torch.zeros(shape, dtype=dtype, device=DEV)
+    Q, S = new(M, H, dtype=torch.uint8), new(M, 1, dtype=torch.float32)
+    A, sA, Hq, sH = dg.swiglu_fp8(torch.randn(M, 2 * H, device=DEV))
+    calls = {
+        "moe_permute": lambda o: dg.moe_permute(x, plan.slot_row, plan.row_slot, Y=o[0]),
+        "moe_permute_fp8": lambda o: dg.moe_permute_fp8(x, plan.slot_row, plan.row_slot, Q=o[0], S=o[1]),
+        "moe_combine": lambda o: dg.moe_combine(new(M, H), plan.slot_row, w, out=o[0]),
+        "moe_combine_bwd": lambda o: dg.moe_combine_bwd(x, new(M, H), plan.slot_row, plan.row_slot, w, dY=o[0],
+                                                        dweights=o[1]),
+        "swiglu_fp8_bwd": lambda o: dg.swiglu_fp8_bwd(new(M, H), Hq, sH, dH=o[0]),
+        "grouped_wgrad_fp8": lambda o: dg.grouped_wgrad_fp8(new(M, H), A, sA, plan.group_offsets, dW=o[0],
+                                                            accumulate=True),
+    }
+    outputs = {"moe_permute": [new(M, H)], "moe_permute_fp8": [Q, S], "moe_combine": [new(T, H)],
+               "moe_combine_bwd": [new(M, H), new(T, k, dtype=torch.float32)], "swiglu_fp8_bwd": [new(M, 2 * H)],
+               "grouped_wgrad_fp8": [new(G, H, H, dtype=torch.float32)]}
+    for name, call in calls.items():
+        before = [t._version for t in outputs[name]]
+        call(outputs[name])
+        assert all(t._version > v for t, v in zip(outputs[name], before)), name
+    leaf = torch.ones(G, H, H, device=DEV, requires_grad=True)
+    dw = outputs["grouped_wgrad_fp8"][0]
+    loss = (leaf * dw).sum()
+    calls["grouped_wgrad_fp8"]([dw])
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    with torch.inference_mode():                               # tensors without a version
+        out = new(T, H)
+        dg.moe_combine(new(M, H), plan.slot_row, w, out=out)
