@@ -198,10 +198,16 @@ PyObject* moe_sort(PyObject*, PyObject* const* a, Py_ssize_t n) {
   check(ids, "ids", {at::kInt, at::kLong});
   const int64_t T = ids.size(0), k = ids.size(1);
   const int G = small(a[1], "num_groups"), align = small(a[2], "align");
-  const int64_t ws = k > INT32_MAX ? -1 : lib.moe_sort_workspace(T, int(k), G);
-  int64_t M = k > INT32_MAX ? -1 : lib.moe_rows(T, int(k), G, align);
-  if (a[3] != Py_None && M >= 0) M = integer(a[3], "rows");
-  if (M < 0 || M > INT32_MAX || ws < 0) return failure(DG_ERR_INVALID_ARG, "dg_moe_sort");
+  // what the sort would refuse is refused before anything is allocated for it
+  int64_t M = k > INT32_MAX ? int64_t(DG_ERR_INVALID_ARG) : lib.moe_rows(T, int(k), G, align);
+  if (M < 0) return failure(M, "dg_moe_sort");
+  const int64_t ws = lib.moe_sort_workspace(T, int(k), G);
+  if (a[3] != Py_None) {
+    const int64_t rows = integer(a[3], "rows");
+    if (rows < M || rows % align != 0) return failure(DG_ERR_INVALID_ARG, "dg_moe_sort");
+    M = rows;
+  }
+  if (M > INT32_MAX) return failure(DG_ERR_INVALID_ARG, "dg_moe_sort");
   // one allocation for the plan: four cost 2 us more
   const Tensor all = create({2 * int64_t(G) + 1 + M + T * k}, at::kInt, ids);
   const Tensor offs = part(all, 0, {G + 1}), counts = part(all, G + 1, {G});

@@ -82,6 +82,14 @@ int check_tokens(int64_t T, int top_k, int64_t M, int64_t H) {
   return DG_OK;
 }
 
+// Slots and experts of the sort.
+int check_sort(int64_t T, int top_k, int num_groups) {
+  if (num_groups < 1) return DG_ERR_INVALID_ARG;
+  const int st = check_tokens(T, top_k, 0, 0);
+  if (st != DG_OK) return st;
+  return num_groups > dg::kSortMaxGroups ? DG_ERR_UNSUPPORTED : DG_OK;
+}
+
 // Slots that one workgroup of the counting sort takes.
 int64_t sort_chunk(int64_t slots) {
   if (slots <= dg::kSortSingle) return ceil_div(std::max<int64_t>(slots, 1), dg::kSortThreads) * dg::kSortThreads;
@@ -102,13 +110,15 @@ int64_t padding_blocks(int64_t M) { return ceil_div(M, 64); }
 extern "C" {
 
 int64_t dg_moe_rows(int64_t T, int top_k, int num_groups, int align) {
-  if (T < 0 || top_k < 1 || num_groups < 1 || (align != 1 && align != 128) || T > kMaxSlots || T * top_k > kMaxSlots)
-    return DG_ERR_INVALID_ARG;
+  if (align != 1 && align != 128) return DG_ERR_INVALID_ARG;
+  const int st = check_sort(T, top_k, num_groups);
+  if (st != DG_OK) return st;
   return rows_of(T, top_k, num_groups, align);
 }
 
 int64_t dg_moe_sort_workspace(int64_t T, int top_k, int num_groups) {
-  if (T < 0 || top_k < 1 || num_groups < 1 || T > kMaxSlots || T * top_k > kMaxSlots) return DG_ERR_INVALID_ARG;
+  const int st = check_sort(T, top_k, num_groups);
+  if (st != DG_OK) return st;
   const int64_t slots = T * top_k;
   return slots <= dg::kSortSingle ? 0 : 4 * ceil_div(slots, sort_chunk(slots)) * num_groups;
 }
@@ -118,10 +128,9 @@ int dg_moe_sort(const void* ids, int ids_dtype, int64_t T, int top_k, int num_gr
                 hipStream_t stream) {
   if (ids_dtype != DG_IDX_I32 && ids_dtype != DG_IDX_I64) return DG_ERR_INVALID_ARG;
   if (align != 1 && align != 128) return DG_ERR_INVALID_ARG;
-  if (num_groups < 1) return DG_ERR_INVALID_ARG;
-  const int st = check_tokens(T, top_k, M_total, 0);
+  if (M_total < 0 || M_total > kMaxDim) return DG_ERR_INVALID_ARG;
+  const int st = check_sort(T, top_k, num_groups);
   if (st != DG_OK) return st;
-  if (num_groups > dg::kSortMaxGroups) return DG_ERR_UNSUPPORTED;
   const int64_t slots = T * top_k;
   if (M_total < rows_of(T, top_k, num_groups, align) || M_total % align != 0) return DG_ERR_INVALID_ARG;
   if (bad(group_offsets, 4) || bad(group_counts, 4)) return DG_ERR_INVALID_ARG;

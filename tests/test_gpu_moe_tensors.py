@@ -86,3 +86,18 @@ def test_written_outputs_change_their_version():
     with torch.inference_mode():                               # tensors without a version
         out = new(T, H)
         dg.moe_combine(new(M, H), plan.slot_row, w, out=out)
+
+
+@pytest.mark.parametrize("args,status", [((1025,), dg.DG_ERR_UNSUPPORTED), ((2 ** 31 - 1,), dg.DG_ERR_UNSUPPORTED),
+                                         ((0,), dg.DG_ERR_INVALID_ARG), ((8, 64), dg.DG_ERR_INVALID_ARG),
+                                         ((8, 128, 128), dg.DG_ERR_INVALID_ARG),
+                                         ((8, 128, 2 ** 31 - 2 ** 20 + 1), dg.DG_ERR_INVALID_ARG),
+                                         ((8, 1, 2 ** 31), dg.DG_ERR_INVALID_ARG)])
+def test_a_refused_sort_allocates_nothing(args, status):
+    ids = torch.zeros(100, 2, dtype=torch.int32, device=DEV)
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    with pytest.raises(dg.DGError) as e:
+        dg.moe_sort(ids, *args)
+    assert e.value.status == status
+    assert torch.cuda.max_memory_allocated() == before
