@@ -127,8 +127,8 @@ __device__ __forceinline__ void wgrad_body(const WgradArgs& p) {
   constexpr int RB = 4096, SB = 1024;            // codes and scales of a stage
   static_assert(BR * BK == RB, "a thread takes 16 codes and their scale");
   static_assert(KI == 4, "the step's schedule");
-  constexpr int DEPTH = 3;                       // stages of everything copied
-  constexpr int X0 = DEPTH * YB, R0 = X0 + 2 * XB, S0 = R0 + DEPTH * RB;
+  constexpr int DEPTH = kSingleStage ? 1 : 3;    // stages of everything copied
+  constexpr int X0 = DEPTH * YB, R0 = X0 + (kSingleStage ? 1 : 2) * XB, S0 = R0 + DEPTH * RB;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[S0 + DEPTH * SB];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -237,6 +237,30 @@ __device__ __forceinline__ void wgrad_body(const WgradArgs& p) {
     for (int i = 0; i < NI; ++i) acc[j][i] = v4f{0.f, 0.f, 0.f, 0.f};
   v8bf fx[KI], fy[NI];
 
+  if constexpr (kSingleStage) {
+    // (uniform: all waves of the workgroup take the same steps)
+    for (int s = 0; s < steps; ++s) {
+      copy_x(s, 0);
+      copy_y(s, 0);
+      wait_vmem();
+      read_raw(0);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) decode_word(w);
+      write_x(0);
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < KI; ++j) fx[j] = read_x(0, j);
+#pragma unroll
+      for (int i = 0; i < NI; ++i) fy[i] = read_y(0, i);
+#pragma unroll
+      for (int j = 0; j < KI; ++j)
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+          acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fx[j], fy[i], acc[j][i], 0, 0, 0);
+      __syncthreads();                            // the stage has been read
+    }
+  }
+
   // Step s multiplies the operands in registers and reads those of step s + 1
   // (whose stages the last barrier has closed) into the registers that the
   // products free; it decodes X of step s + 2 into the stage that step s used,
@@ -248,7 +272,7 @@ __device__ __forceinline__ void wgrad_body(const WgradArgs& p) {
   // goes first, so that one's stores overlap the other's products (8 experts of
   // 1024 rows, 4096 x 4096 FP32: 344 -> 332 us)
   if ((blockIdx.x >> 8) & 1) __builtin_amdgcn_s_setprio(1);
-  if (steps > 0) {
+  if (!kSingleStage && steps > 0) {
     // X of steps 0 and 1 through registers, everything else of the first steps
     // behind it: one wait for memory before the first product
     u32x4 first[2];
