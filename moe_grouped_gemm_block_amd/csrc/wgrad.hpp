@@ -15,7 +15,8 @@
 // so that one's products cover the other's waits and stores.  dY goes straight
 // into LDS; X goes there as codes, each thread's own 16 bytes and scale, two
 // steps later through registers and back as BF16, one conversion per element and
-// tile.  Copies run three steps ahead and are counted by hand.
+// tile.  Copies are issued three steps (dY) and five (X) ahead into rotating slots;
+// each lands by the end of the step after the one that issued it.
 //
 // The results leave through LDS in whole lines and past the caches (non-temporal
 // stores), which keeps the operands in L2: 8 experts of 1024 rows with FP32
@@ -266,15 +267,18 @@ __device__ __forceinline__ void wgrad_body(const WgradArgs& p) {
   // products free; it decodes X of step s + 2 into the stage that step s used,
   // then copies X of step s + 5 and dY of step s + 3.  Past the last row
   // everything reads zeros.  The copies are counted by hand (G per step, X
-  // before dY), never waited for all at once.
+  // before dY): a step's own stay in flight over its end, those of the step before
+  // have landed there, X of step s + 4 with them, three steps before its use.
   constexpr int G = 2 + YC;
-  // Workgroups start 256 at a time, one per CU: of the two that share a CU one
-  // goes first, so that one's stores overlap the other's products (8 experts of
-  // 1024 rows, 4096 x 4096 FP32: 344 -> 332 us)
+  // The first workgroups start 256 at a time, one per CU: of the two that share a
+  // CU one goes first, so that one's stores overlap the other's products (8 experts
+  // of 1024 rows, 4096 x 4096 FP32: 344 -> 332 us).  Later ones start where a place
+  // is free, so two of a CU may have the same priority.
   if ((blockIdx.x >> 8) & 1) __builtin_amdgcn_s_setprio(1);
   if (!kSingleStage && steps > 0) {
     // X of steps 0 and 1 through registers, everything else of the first steps
-    // behind it: one wait for memory before the first product
+    // behind it: one wait for memory before the first product.  (The compiler's
+    // waits for these loads do not know of the copies behind them and wait for all.)
     u32x4 first[2];
     float first_s[2];
 #pragma unroll
@@ -300,7 +304,7 @@ __device__ __forceinline__ void wgrad_body(const WgradArgs& p) {
       for (int w = 0; w < 4; ++w) decode_word(w);
       write_x(t);
     }
-    wait_vmem_n<G>();                             // dY of steps 0 and 1
+    wait_vmem_n<G>();                             // dY of steps 0 and 1, whatever the compiler waited for
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < KI; ++j) fx[j] = read_x(0, j);
@@ -312,11 +316,7 @@ __device__ __forceinline__ void wgrad_body(const WgradArgs& p) {
       const uint32_t xst = (s + 1) & 1;
 #pragma unroll
       for (int j = 0; j < KI; ++j) {
-        if (j == 0) {
-          // X of step s + 2: behind it are dY of s .. s + 2 and X of s + 3, s + 4
-          wait_vmem_n<2 * G + YC>();
-          read_raw(c2);
-        }
+        if (j == 0) read_raw(c2);
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
           acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fx[j], fy[i], acc[j][i], 0, 0, 0);
@@ -333,7 +333,7 @@ __device__ __forceinline__ void wgrad_body(const WgradArgs& p) {
           copy_y(s + 3, a);
         }
       }
-      wait_vmem_n<G>();                           // dY of step s + 2; behind it X of s + 5 and dY of s + 3
+      wait_vmem_n<G>();                           // all but X of step s + 5 and dY of s + 3
       __syncthreads();
       const uint32_t t = a;
       a = b;
