@@ -3,16 +3,16 @@
     python -m moe_grouped_gemm_block_amd.build
 
 Each source under csrc/ (the host side, one translation unit per pair of operand
-formats, see csrc/kernels.hpp, and the operators around the products) is compiled to an object in parallel,
-then the objects are linked into libdg.so; the torch binding of the operators around the
-products (csrc/binding.cpp, host code) becomes the extension module _dg_torch.so.  Packed FP32 instructions are
-disabled for the device code (the host pass warns that it does not know the
-feature; that warning is harmless).
+formats, see csrc/kernels.hpp, and the operators around the products) is compiled
+to an object in parallel, then the objects are linked into libdg.so; the torch
+binding of the operators around the products (csrc/binding.cpp, host code, the
+compiler in CXX or g++) becomes the extension module _dg_torch.so.  Packed FP32
+instructions are disabled for the device code (the host pass warns that it does
+not know the feature; that warning is harmless).
 """
 from __future__ import annotations
 
 import concurrent.futures
-import importlib.util
 import os
 import shutil
 import subprocess
@@ -54,14 +54,22 @@ def link_command(objs: list[str], out: str) -> list[str]:
     return [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", out]
 
 
-def binding_command(out: str) -> list[str]:
-    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
-    headers = os.path.join(torch, "include")
-    return [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
-            "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1", "-D_GLIBCXX_USE_CXX11_ABI=1", "-I", INCLUDE,
+def binding_command(out: str) -> list[str] | None:
+    """None where there is no ROCm build of torch: the libraries do without."""
+    try:
+        import torch
+    except ImportError:
+        return None
+    if torch.version.hip is None:
+        return None
+    home = os.path.dirname(torch.__file__)
+    headers = os.path.join(home, "include")
+    return [os.environ.get("CXX") or shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+            "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I", INCLUDE,
             "-isystem", headers, "-isystem", os.path.join(headers, "torch", "csrc", "api", "include"),
             "-isystem", sysconfig.get_paths()["include"], "-isystem", "/opt/rocm/include",
-            os.path.join(CSRC, "binding.cpp"), "-o", out, "-L", os.path.join(torch, "lib"),
+            os.path.join(CSRC, "binding.cpp"), "-o", out, "-L", os.path.join(home, "lib"),
             "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python", "-ldl"]
 
 
@@ -74,16 +82,22 @@ def _run(cmd: list[str]) -> str:
 
 
 def build(verbose: bool = True) -> str:
-    """Build the torch binding _dg_torch.so, libdg.so and its single-stage twin libdg_stages1.so (the same
+    """Build libdg.so and its single-stage twin libdg_stages1.so (the same
     library compiled with -DDG_STAGES=1: every GEMM pipeline with one LDS
-    stage, a debugging aid whose results must equal libdg.so's bit for bit);
-    returns the path of libdg.so."""
+    stage, a debugging aid whose results must equal libdg.so's bit for bit),
+    and, where torch is installed, its binding _dg_torch.so; returns the path of
+    libdg.so."""
     with tempfile.TemporaryDirectory(prefix="dg_build_") as tmp:
         jobs_list = []
         for stages, lib in ((2, LIB), (1, LIB_STAGES1)):
             objs = [os.path.join(tmp, f"s{stages}_" + os.path.splitext(s)[0] + ".o") for s in SOURCES]
             jobs_list.append((lib, objs, [compile_command(s, o, stages) for s, o in zip(SOURCES, objs)]))
-        cmds = [c for _, _, cs in jobs_list for c in cs] + [binding_command(BINDING + ".tmp")]
+        cmds = [c for _, _, cs in jobs_list for c in cs]
+        binding = binding_command(BINDING + ".tmp")
+        if binding is not None:
+            cmds.append(binding)
+        else:
+            print("no ROCm build of torch: the torch binding (_dg_torch.so) is left out", file=sys.stderr)
         if verbose:
             for c in cmds:
                 print(" ".join(c), flush=True)
@@ -94,7 +108,7 @@ def build(verbose: bool = True) -> str:
             warnings.append(_run(link_command(objs, lib + ".tmp")))
     if verbose and any(w.strip() for w in warnings):
         print("\n".join(w for w in warnings if w.strip()), file=sys.stderr)
-    for lib in [lib for lib, _, _ in jobs_list] + [BINDING]:
+    for lib in [lib for lib, _, _ in jobs_list] + ([BINDING] if binding is not None else []):
         os.replace(lib + ".tmp", lib)
     return LIB
 
