@@ -82,26 +82,21 @@ def lib() -> ctypes.CDLL:
         L.dg_grouped_gemm_fp8_segments.restype = ci
         L.dg_quantize_fp8_blockscaled.argtypes = [vp, ci, vp, vp, i64, i64, ci, vp]
         L.dg_quantize_fp8_blockscaled.restype = ci
-        L.dg_moe_sort.argtypes = [vp, ci, i64, ci, ci, ci, i64, vp, vp, vp, vp, vp, vp]
-        L.dg_moe_sort.restype = ci
-        L.dg_moe_rows.argtypes = [i64, ci, ci, ci]
-        L.dg_moe_rows.restype = i64
-        L.dg_moe_sort_workspace.argtypes = [i64, ci, ci]
-        L.dg_moe_sort_workspace.restype = i64
-        L.dg_moe_permute.argtypes = [vp, ci, vp, vp, vp, i64, ci, i64, i64, vp]
-        L.dg_moe_permute.restype = ci
-        L.dg_moe_permute_fp8.argtypes = [vp, ci, vp, vp, ci, vp, vp, i64, ci, i64, i64, vp]
-        L.dg_moe_permute_fp8.restype = ci
-        L.dg_moe_combine.argtypes = [vp, ci, vp, vp, vp, i64, ci, i64, i64, vp]
-        L.dg_moe_combine.restype = ci
-        L.dg_moe_combine_bwd.argtypes = [vp, vp, ci, vp, vp, vp, vp, vp, i64, ci, i64, i64, vp]
-        L.dg_moe_combine_bwd.restype = ci
-        L.dg_swiglu_fp8.argtypes = [vp, ci, vp, vp, vp, vp, i64, i64, vp]
-        L.dg_swiglu_fp8.restype = ci
-        L.dg_swiglu_fp8_bwd.argtypes = [vp, ci, vp, vp, vp, i64, i64, vp]
-        L.dg_swiglu_fp8_bwd.restype = ci
-        L.dg_grouped_wgrad_fp8.argtypes = [vp, vp, vp, vp, vp, ci, i64, i64, i64, vp, ci, ci, vp]
-        L.dg_grouped_wgrad_fp8.restype = ci
+        around = {
+            "dg_moe_sort": (ci, [vp, ci, i64, ci, ci, ci, i64, vp, vp, vp, vp, vp, vp]),
+            "dg_moe_rows": (i64, [i64, ci, ci, ci]),
+            "dg_moe_sort_workspace": (i64, [i64, ci, ci]),
+            "dg_moe_permute": (ci, [vp, ci, vp, vp, vp, i64, ci, i64, i64, vp]),
+            "dg_moe_permute_fp8": (ci, [vp, ci, vp, vp, ci, vp, vp, i64, ci, i64, i64, vp]),
+            "dg_moe_combine": (ci, [vp, ci, vp, vp, vp, i64, ci, i64, i64, vp]),
+            "dg_moe_combine_bwd": (ci, [vp, vp, ci, vp, vp, vp, vp, vp, i64, ci, i64, i64, vp]),
+            "dg_swiglu_fp8": (ci, [vp, ci, vp, vp, vp, vp, i64, i64, vp]),
+            "dg_swiglu_fp8_bwd": (ci, [vp, ci, vp, vp, vp, i64, i64, vp]),
+            "dg_grouped_wgrad_fp8": (ci, [vp, vp, vp, vp, vp, ci, i64, i64, i64, vp, ci, ci, vp]),
+        }
+        for name, (result, arguments) in around.items():
+            if hasattr(L, name):                  # a library of an earlier build may lack it; calling it then raises
+                getattr(L, name).restype, getattr(L, name).argtypes = result, arguments
         L.dg_status_string.argtypes = [ci]
         L.dg_status_string.restype = ctypes.c_char_p
         _lib = L
