@@ -267,8 +267,9 @@ int dg_grouped_wgrad_fp8(const void* dY, const void* X, const float* sX, const i
                   dW, num_groups, int(M_total), int(N), int(K), int(ceil_div(K, 128)), 0, 0, 0, accumulate};
   const bool bf16 = out_dtype == DG_OUT_BF16;
   // 256 x 128 tiles from more than one per CU (256) on, 128 x 128 below (FP32,
-  // 256 x 128 against 128 x 128: 64 tiles of 1024 rows 26.1 / 20.8 us, 256 of 256
-  // rows 17.8 / 17.5, 384 of 256 rows 23.7 / 24.6, 512 of 512 rows 29.6 / 35.5)
+  // 256 x 128 against 128 x 128: 64 tiles of 1024 rows 23.9 / 17.7 us, 256 of 256
+  // rows 15.2 / 13.2, 320 of 1024 rows 36.0 / 38.7, 384 of 256 rows 19.6 / 19.6, 512
+  // of 512 rows 28.6 / 33.2)
   const bool big = num_groups * ceil_div(N, 256) * ceil_div(K, 128) > 256;
   a.n_tiles = int(ceil_div(N, big ? 256 : 128));
   a.k_tiles = int(ceil_div(K, 128));

@@ -13,7 +13,7 @@
 // exact BF16 values (which the weight gradient's matrix product relies on).
 //
 // Both passes are bound by memory: forward 4 bytes in and 3 out per element
-// pair (9216 rows of 2 x 4096 in BF16: 45.6 us, 5.9 TB/s; a copy reaches 5.3),
+// pair (9216 rows of 2 x 4096 in BF16: 45.9 us, 5.8 TB/s; a copy reaches 5.3),
 // backward 4 in and 4 out (6.7 TB/s).  An 8-lane group takes one block of 128
 // columns, 16 values of g, u and a per lane in registers; the block maxima are
 // reduced by lane permutations, nothing goes through LDS.  (Eight values per
@@ -211,7 +211,7 @@ __device__ __forceinline__ void silu_mul_bwd_f64(float d, double g, double u, fl
 // 1/8 reach them, 448 / 8 = 56, so others are not searched).  NaN goes through
 // either: comparisons that choose are false for it, and nothing clamps.
 // dA and dH past the caches (non-temporal), the codes' pieces of 8 bytes not: 9216
-// rows of 2 x 4096 in BF16 45.5 us, 6.7 TB/s (all plain 52.7, all non-temporal
+// rows of 2 x 4096 in BF16 45.4 us, 6.7 TB/s (all plain 52.7, all non-temporal
 // 47.4).
 template <bool BF16>
 __device__ __forceinline__ void swiglu_bwd_body(const SwigluBwdArgs& p) {

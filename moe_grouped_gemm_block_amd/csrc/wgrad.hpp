@@ -23,20 +23,27 @@
 // results 333 -> 318 us, 64 uneven experts with BF16 results 277 -> 258 us
 // (non-temporal stores of half lines were slower, 353 and 295).
 //
-// What bounds it: power.  8 experts of 1024 rows, N = K = 4096, FP32: 312 us, 880
-// TFLOP/s, with the clock down to 2.0 GHz; the 537 MB of results take 93 us by
-// themselves, further rows cost 1.2 to 1.3 PFLOP/s, and a workgroup made to wait
-// between its stores, or made to start later, changes nothing (a library product
-// of BF16 operands of this form reaches 1.23 PFLOP/s, zeros in place of random
-// operands 1.46, the matrix cores alone with operands in registers 2.0).  64
-// experts with 16384 rows unevenly, N = K = 2048, BF16: 250 us at 2.25 GHz, most
-// tiles having two to eight steps: the first loads and the stores of a tile,
-// covered by one other workgroup only.  What was slower: 128 x 128 tiles, plain
-// LDS reads and one stage 967 and 627 us; one workgroup of 256 x 256 tiles per CU,
-// with a third less LDS traffic, 340 and 303; 512 workgroups that go through
-// shares of the tiles, loading the next one before the stores of the last, 329 and
-// 304 (where rows are even, 134 instead of 151 us for 256 each); the experts in
-// order of their rows, the same on average.
+// What bounds it.  8 experts of 1024 rows, N = K = 4096: 311 to 322 us with FP32
+// results (850 to 885 TFLOP/s), 282 to 289 with BF16 ones.  That is nearly the sum
+// of the stores (94 and 46 us without rows) and of the products (further rows cost
+// 1.23 PFLOP/s): a tile's stores overlap little with other tiles' products.  The
+// matrix units are busy 0.4 of the cycles.  Zeros as operands save 40 us, by the
+// clock, which falls from 2.1 to 1.85 GHz over nine launches; a workgroup made to
+// wait between its stores, or to start later, changes nothing.  A library's products
+// of BF16 operands of this shape take 303 to 315 us one after another with BF16
+// results, 358 to 369 with FP32 ones, 263 to 271 batched on operands laid out for
+// it.  64 experts with 16384 rows unevenly, N = K = 2048, BF16: 243 to 270 us by
+// their routing, most tiles having two to eight steps: the first loads and the
+// stores of a tile, covered by one other workgroup only.  Few tiles: 64 of 128 x 128
+// with 1024 rows 16.7 us, with 16384 rows 194, the same as 16 or 128 tiles, since a
+// workgroup takes all rows.  Added to FP32 gradients instead of stored: 452 us.
+//
+// What was slower: 128 x 128 tiles, plain LDS reads and one stage 967 and 627 us
+// (8 and 64 experts); one workgroup of 256 x 256 tiles per CU, with a third less LDS
+// traffic, 340 and 303; 512 workgroups that go through shares of the tiles, loading
+// the next one before the stores of the last, 329 and 304 (where rows are even, 134
+// instead of 151 us for 256 each); the experts in order of their rows, the same on
+// average.
 #pragma once
 
 #include <hip/hip_runtime.h>

@@ -410,7 +410,9 @@ def quantize_fp8_blockscaled(X, block_rows=128, Q=None, S=None, stream=None):
 # ---------------------------------------------------------------- around the products
 #
 # Checks of the tensors, output tensors and the current stream are native code
-# (csrc/binding.cpp, the module _dg_torch), which then makes the calls above.
+# (csrc/binding.cpp, the module _dg_torch), which then makes the calls above.  Like
+# the helpers above, these record nothing for autograd: outputs are detached, and a
+# layer calls the forward and backward operators itself (examples/moe_layer.py).
 
 class MoEPlan(NamedTuple):
     """What moe_sort finds out about one batch (device int32 tensors)."""
