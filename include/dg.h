@@ -471,6 +471,137 @@ int dg_grouped_wgrad_fp8(const void* dY, const void* X, const float* sX, const i
                          const int32_t* group_counts, int num_groups, int64_t M_total, int64_t N,
                          int64_t K, void* dW, int out_dtype, int accumulate, hipStream_t stream);
 
+/*
+ * The operators that make the mixture-of-experts layer a block of a model: the
+ * router in front of it, the norms around it, and the clipping of its gradients.
+ * The shared conventions above apply: caller-owned device memory, asynchronous on
+ * `stream`, host-side argument checks before any HIP call, nothing atomic whose
+ * order shows, results bitwise repeatable, no allocation, capturable into a HIP
+ * graph.  Outputs must not overlap inputs or each other unless a call says so.
+ */
+typedef enum {
+  DG_SCORE_SOFTMAX = 0,  /* s = p = exp(x) / sum exp(x) */
+  DG_SCORE_SIGMOID = 1   /* s = 1 / (1 + exp(-x)), p = s / sum s */
+} dg_score;
+
+/*
+ * Router.  Token t's logits x [E] give its scores s and probabilities p (above),
+ * its choices and their weights, and the load of the experts:
+ *
+ *   logits      : [T][E] of `dtype` (dg_in_dtype); an expert with -inf is closed to
+ *                 the token.  NaN ranks above every number.
+ *   bias        : float32 [E] or null.  With it the choice goes by s + bias,
+ *                 compared in 64 bits, without it by x; weights know no bias.  An
+ *                 expert whose bias is -inf is closed.
+ *   mask        : bytes [T], 0 for a row that holds no token, or null
+ *   ids         : int32 [T][top_k], the top_k largest in falling order, the lower
+ *                 index first of equals; -1 where no expert is left that is open
+ *   weights     : float32 [T][top_k], scale s_j, or scale s_j / (the chosen scores'
+ *                 sum) if renormalise = 1; 0 for the id -1
+ *   counts      : int32 [E], tokens that chose e
+ *   prob_sums   : float32 [E], sum of p_e over the tokens with a choice
+ *   routed      : int32 [1], their number n
+ *   loss        : float32 [1], E / (top_k n^2) sum_e counts_e prob_sums_e (the
+ *                 balance loss: 1 where both are even), 0 if n = 0
+ *   workspace   : dg_moe_route_workspace() bytes, in use until the work is done
+ *
+ * counts, prob_sums, routed and loss are all null where no load is wanted (decode);
+ * workspace is then not used.  Shares whose scores all underflow are those of the
+ * real numbers.  A row that holds NaN, or +inf under softmax, gives NaN weights and
+ * sums and ids within [0, E).  E up to 1024, top_k up to 64 and at most 2^30 slots
+ * (DG_ERR_UNSUPPORTED); top_k > E, a scale that is not finite -> DG_ERR_INVALID_ARG.
+ * T == 0 is no empty work where a load is wanted.
+ */
+int64_t dg_moe_route_workspace(int64_t T, int64_t E, int top_k);
+int dg_moe_route(const void* logits, int dtype, const float* bias, const uint8_t* mask, int64_t T, int64_t E,
+                 int top_k, int score, int renormalise, float scale, int32_t* ids, float* weights,
+                 int32_t* counts, float* prob_sums, int32_t* routed, float* loss, void* workspace,
+                 hipStream_t stream);
+
+/*
+ * Its gradient: dlogits [T][E] of `dtype` from dweights float32 [T][top_k] and dloss
+ * float32 [1], the gradient of the loss.  Choices and counts are constants; counts
+ * and routed may be those of several devices added up.  counts, routed and dloss are
+ * all null where the loss takes no part.  ids outside [0, E) are no choices (their
+ * dweights are not used); a row without choices gives zeros, its logits are not read.
+ */
+int dg_moe_route_bwd(const float* dweights, const void* logits, int dtype, const int32_t* ids,
+                     const int32_t* counts, const int32_t* routed, const float* dloss, int64_t T, int64_t E,
+                     int top_k, int score, int renormalise, float scale, void* dlogits, hipStream_t stream);
+
+typedef enum {
+  DG_GATE_NONE = 0,
+  DG_GATE_CHANNEL = 1,   /* gate float32 [H] */
+  DG_GATE_TOKEN = 2      /* gate float32 [T] */
+} dg_gate;
+
+/*
+ * The residual stream past a block, and the norm before the next one.  With
+ * rms(v, w) = w v / sqrt(mean(v^2) + eps):
+ *
+ *   R_out = R + alpha gate rms(Y, w_post)      N = rms(R_out, w_pre)
+ *
+ *   R, R_out    : [T][H] of r_dtype; Y, N : [T][H] of dtype (dg_in_dtype each)
+ *   Y           : null: no block before, R_out (then null too) is R
+ *   w_post      : float32 [H], or null: Y as it is.  gate null: none.
+ *   w_pre       : float32 [H], or null: no norm (N, Q, S null too)
+ *   N           : values, and/or
+ *   Q, S        : E4M3FN codes [T][H] and float32 scales [T][ceil(H/128)] of N as a
+ *                 real number, one per row and 128 columns, scale_mode as in
+ *                 dg_moe_permute_fp8 (the A operand of the products with sa_rows =
+ *                 1); null: none.  H a multiple of 16 (DG_ERR_UNSUPPORTED).
+ *
+ * N is that of the sum before its rounding to r_dtype.  Sums are held in 64 bits.
+ * Any H from 1 to 2^22 (above: DG_ERR_UNSUPPORTED); all matrices and w_post, w_pre
+ * and a channel's gate are 16-byte aligned.  eps > 0; eps and alpha finite
+ * (DG_ERR_INVALID_ARG).  T == 0 is a no-op.
+ */
+int dg_residual_norm(const void* R, int r_dtype, const void* Y, int dtype, const float* w_post,
+                     const float* gate, int gate_kind, float alpha, const float* w_pre, float eps, void* R_out,
+                     void* N, void* Q, float* S, int scale_mode, int64_t T, int64_t H, hipStream_t stream);
+
+/*
+ * Its gradients, from those of R_out (dR, null: zeros) and N (dN, with w_pre), and
+ * from R, the stream AFTER the block as dg_residual_norm stored it (R itself without
+ * a block; not read without w_pre):
+ *
+ *   dR_out  : [T][H] of r_dtype, the gradient of the stream before the block
+ *   dY      : [T][H] of dtype, with Y
+ *   dw_post, dgate, dw_pre : float32, of the shapes of what they belong to; null
+ *             exactly where that is null
+ *   workspace : dg_residual_norm_bwd_workspace(T, H, sums) bytes, 16-byte aligned,
+ *             where sums counts w_pre, and w_post or a channel's gate (0 to 2)
+ *
+ * T == 0 is no empty work: the weights' gradients are written (zeros).
+ */
+int64_t dg_residual_norm_bwd_workspace(int64_t T, int64_t H, int sums);
+int dg_residual_norm_bwd(const void* dR, const void* dN, const void* R, int r_dtype, const void* Y, int dtype,
+                         const float* w_post, const float* gate, int gate_kind, float alpha,
+                         const float* w_pre, float eps, void* dR_out, void* dY, float* dw_post, float* dgate,
+                         float* dw_pre, int64_t T, int64_t H, void* workspace, hipStream_t stream);
+
+/*
+ * The norm of many gradients, norm float32 [1] = sqrt(sum of the squares of all
+ * elements), squares and sums in 64 bits.  grads, sizes (elements) and dtypes
+ * (dg_in_dtype) are HOST arrays of `count` entries, read before the call returns (a
+ * captured graph holds the addresses in them).  A tensor needs the alignment of its
+ * elements (16 bytes is faster) and may be empty; a tensor named twice counts twice.
+ * workspace: dg_grad_norm_workspace() bytes, 8-byte aligned.  count == 0 gives 0.
+ */
+int64_t dg_grad_norm_workspace(const int64_t* sizes, const int* dtypes, int count);
+int dg_grad_norm(const void* const* grads, const int64_t* sizes, const int* dtypes, int count, float* norm,
+                 void* workspace, hipStream_t stream);
+
+/*
+ * Clipping: outs[i] = grads[i] min(1, max_norm / norm), with norm float32 [1] on the
+ * device.  outs[i] may be grads[i] (of the same type then) and must not overlap
+ * anything else in the lists (DG_ERR_INVALID_ARG).  A norm of NaN gives NaN, an
+ * infinite one zeros and, for infinite elements, NaN.  max_norm finite and positive.
+ */
+int dg_clip_grads(const void* const* grads, const int64_t* sizes, const int* dtypes, int count,
+                  const float* norm, float max_norm, void* const* outs, const int* out_dtypes,
+                  hipStream_t stream);
+
 /* Static, NUL-terminated description of a dg_status value. */
 const char* dg_status_string(int status);
 

@@ -28,7 +28,7 @@ LIB = os.path.join(PKG, "libdg.so")
 LIB_STAGES1 = os.path.join(PKG, "libdg_stages1.so")
 BINDING = os.path.join(PKG, "_dg_torch.so")
 SOURCES = ["dg_api.hip", "kernels_e4m3.hip", "kernels_e4m3_e5m2.hip", "kernels_e5m2_e4m3.hip",
-           "kernels_e5m2.hip", "kernels_wgrad.hip", "moe_api.hip"]
+           "kernels_e5m2.hip", "kernels_wgrad.hip", "moe_api.hip", "block_api.hip"]
 ARCH = os.environ.get("DG_OFFLOAD_ARCH", "gfx950")
 HARMLESS = "packed-fp32-ops' is not a recognized feature"
 

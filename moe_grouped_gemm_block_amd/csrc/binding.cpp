@@ -1,4 +1,4 @@
-// The torch side of the mixture-of-experts operators: argument checks, output
+// The torch side of the operators around the products: argument checks, output
 // tensors and the current stream, then the C calls of dg.h.  dg.py's functions of
 // the same names call these; in Python the same checks and allocations take as
 // long again as the kernel launch (combine: 7.6 us a call, here 3.8).
@@ -12,6 +12,7 @@
 
 #include <initializer_list>
 #include <string>
+#include <vector>
 
 #include "dg.h"
 
@@ -31,6 +32,16 @@ struct Library {
   decltype(&dg_swiglu_fp8) swiglu_fp8;
   decltype(&dg_swiglu_fp8_bwd) swiglu_fp8_bwd;
   decltype(&dg_grouped_wgrad_fp8) grouped_wgrad_fp8;
+  // null where an earlier build of the library lacks them
+  decltype(&dg_moe_route_workspace) moe_route_workspace;
+  decltype(&dg_moe_route) moe_route;
+  decltype(&dg_moe_route_bwd) moe_route_bwd;
+  decltype(&dg_residual_norm) residual_norm;
+  decltype(&dg_residual_norm_bwd_workspace) residual_norm_bwd_workspace;
+  decltype(&dg_residual_norm_bwd) residual_norm_bwd;
+  decltype(&dg_grad_norm_workspace) grad_norm_workspace;
+  decltype(&dg_grad_norm) grad_norm;
+  decltype(&dg_clip_grads) clip_grads;
 } lib;
 PyObject* dg_error = nullptr;      // dg.DGError
 
@@ -153,6 +164,42 @@ int small(PyObject* o, const char* name) {
 
 void arguments(Py_ssize_t n, Py_ssize_t want) {
   if (n != want) type_error("expected " + std::to_string(want) + " arguments, got " + std::to_string(n));
+}
+
+float real(PyObject* o, const char* name) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) {
+    PyErr_Clear();
+    type_error(std::string(name) + " must be a number");
+  }
+  return float(v);
+}
+
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw python_error();
+  return v != 0;
+}
+
+// The tensor `o`, checked, or null for None; its address.
+const Tensor* optional(PyObject* o, const char* name) { return o == Py_None ? nullptr : &tensor(o, name); }
+const float* weights_of(PyObject* o, const char* name, at::IntArrayRef shape) {
+  const Tensor* t = optional(o, name);
+  if (!t) return nullptr;
+  check(*t, name, {at::kFloat}, shape);
+  return static_cast<const float*>(t->data_ptr());
+}
+
+// One element on the device, whatever its dimensions.
+const void* scalar(const Tensor& t, const char* name, ScalarType dtype) {
+  check(t, name, {dtype});
+  if (t.numel() != 1) value_error(std::string(name) + " must have one element");
+  return t.data_ptr();
+}
+
+template <typename F>
+void need(F f, const char* name) {
+  if (!f) raise(PyExc_RuntimeError, std::string("the library lacks ") + name + ": build it again");
 }
 
 hipStream_t stream() { return c10::hip::getCurrentHIPStream().stream(); }
@@ -377,6 +424,254 @@ PyObject* grouped_wgrad_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// moe_route(logits, top_k, score, renormalise, scale, bias, mask, balance)
+PyObject* moe_route(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arguments(n, 8);
+  need(lib.moe_route, "dg_moe_route");
+  const Tensor& x = tensor(a[0], "logits");
+  const int code = check_values(x, "logits"), k = small(a[1], "top_k"), score = small(a[2], "score");
+  const bool renormalise = truth(a[3]), balance = truth(a[7]);
+  const float scale = real(a[4], "scale");
+  const int64_t T = x.size(0), E = x.size(1);
+  const float* bias = weights_of(a[5], "bias", {E});
+  const uint8_t* mask = nullptr;
+  if (a[6] != Py_None) {
+    const Tensor& m = tensor(a[6], "mask");
+    check(m, "mask", {at::kBool, at::kByte}, {T});
+    mask = static_cast<const uint8_t*>(m.data_ptr());
+  }
+  // what the call would refuse is refused before anything is allocated for it
+  const int64_t ws = lib.moe_route_workspace(T, E, k);
+  if (ws < 0) return failure(ws, "dg_moe_route");
+  const Tensor ids = create({T, k}, at::kInt, x), weights = create({T, k}, at::kFloat, x);
+  Tensor counts, sums, routed, loss, work;
+  if (balance) {
+    const Tensor ints = create({E + 1}, at::kInt, x), floats = create({E + 1}, at::kFloat, x);
+    counts = part(ints, 0, {E});
+    routed = part(ints, E, {});
+    sums = part(floats, 0, {E});
+    loss = part(floats, E, {});
+    work = create({ws}, at::kByte, x);
+  }
+  const int st = lib.moe_route(x.data_ptr(), code, bias, mask, T, E, k, score, renormalise, scale, data<int32_t>(ids),
+                               data<float>(weights), balance ? data<int32_t>(counts) : nullptr,
+                               balance ? data<float>(sums) : nullptr, balance ? data<int32_t>(routed) : nullptr,
+                               balance ? data<float>(loss) : nullptr, balance ? work.data_ptr() : nullptr, stream());
+  if (st != DG_OK) return failure(st, "dg_moe_route");
+  return tuple(ids, weights, counts, sums, routed, loss);
+  END_HANDLE_TH_ERRORS
+}
+
+// moe_route_bwd(dweights, logits, ids, score, renormalise, scale, dloss, counts, routed, dlogits)
+PyObject* moe_route_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arguments(n, 10);
+  need(lib.moe_route_bwd, "dg_moe_route_bwd");
+  const Tensor &dw = tensor(a[0], "dweights"), &x = tensor(a[1], "logits"), &ids = tensor(a[2], "ids");
+  const int code = check_values(x, "logits"), score = small(a[3], "score");
+  const bool renormalise = truth(a[4]);
+  const float scale = real(a[5], "scale");
+  const int64_t T = x.size(0), E = x.size(1);
+  if (ids.dim() != 2 || ids.size(0) != T) value_error("ids has shape " + shape_of(ids.sizes()) + ", expected (" +
+                                                      std::to_string(T) + ", top_k)");
+  check(ids, "ids", {at::kInt});
+  const int k = int(std::min<int64_t>(ids.size(1), INT32_MAX));
+  check(dw, "dweights", {at::kFloat}, {T, k});
+  const float* dloss = nullptr;
+  const int32_t *counts = nullptr, *routed = nullptr;
+  if (const Tensor* t = optional(a[6], "dloss")) {
+    dloss = static_cast<const float*>(scalar(*t, "dloss", at::kFloat));
+    if (a[7] == Py_None || a[8] == Py_None) value_error("dloss needs counts and routed");
+    const Tensor &c = tensor(a[7], "counts"), &r = tensor(a[8], "routed");
+    check(c, "counts", {at::kInt}, {E});
+    counts = data<int32_t>(c);
+    routed = static_cast<const int32_t*>(scalar(r, "routed", at::kInt));
+  }
+  const int64_t refused = lib.moe_route_workspace(T, E, k);
+  if (refused < 0) return failure(refused, "dg_moe_route_bwd");
+  const Tensor dx = output(a[9], "dlogits", {T, E}, x.scalar_type(), x);
+  const int st = lib.moe_route_bwd(data<float>(dw), x.data_ptr(), code, data<int32_t>(ids), counts, routed, dloss, T, E,
+                                   k, score, renormalise, scale, dx.data_ptr(), stream());
+  if (st != DG_OK) return failure(st, "dg_moe_route_bwd");
+  return wrap(dx);
+  END_HANDLE_TH_ERRORS
+}
+
+int dtype_code(const Tensor& t) { return t.scalar_type() == at::kBFloat16 ? DG_IN_BF16 : DG_IN_F32; }
+
+// A gate's kind by its shape: [H] by channel, [T][1] by token.
+int gate_of(PyObject* o, int64_t T, int64_t H, const float** gate) {
+  *gate = nullptr;
+  const Tensor* t = optional(o, "gate");
+  if (!t) return DG_GATE_NONE;
+  const bool channel = t->dim() == 1 && t->size(0) == H, token = t->dim() == 2 && t->size(0) == T && t->size(1) == 1;
+  if (!channel && !token)
+    value_error("gate has shape " + shape_of(t->sizes()) + ", expected " + shape_of({H}) + " or " + shape_of({T, 1}));
+  check(*t, "gate", {at::kFloat});
+  *gate = static_cast<const float*>(t->data_ptr());
+  return channel ? DG_GATE_CHANNEL : DG_GATE_TOKEN;
+}
+
+// residual_norm(R, Y, w_post, gate, alpha, w_pre, eps, values, scale mode or -1, dtype or -1)
+PyObject* residual_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arguments(n, 10);
+  need(lib.residual_norm, "dg_residual_norm");
+  const Tensor& R = tensor(a[0], "R");
+  const int r_code = check_values(R, "R");
+  const int64_t T = R.size(0), H = R.size(1);
+  if (H < 1) return failure(DG_ERR_INVALID_ARG, "dg_residual_norm");   // (its weights have no addresses)
+  const Tensor* Y = optional(a[1], "Y");
+  int code = small(a[9], "dtype");
+  if (Y) {
+    check(*Y, "Y", {at::kBFloat16, at::kFloat}, {T, H});
+    if (code != -1 && code != dtype_code(*Y)) value_error("dtype is Y's where there is Y");
+    code = dtype_code(*Y);
+  }
+  const float *w_post = weights_of(a[2], "w_post", {H}), *w_pre = weights_of(a[5], "w_pre", {H}), *gate;
+  const int kind = gate_of(a[3], T, H, &gate), mode = small(a[8], "codes");
+  const float alpha = real(a[4], "alpha"), eps = real(a[6], "eps");
+  const bool values = truth(a[7]);
+  if (!Y && (w_post || kind != DG_GATE_NONE)) value_error("w_post and gate need Y");
+  if (!Y && !w_pre) value_error("without Y there must be w_pre");
+  if (w_pre && !values && mode < 0) value_error("w_pre asks for values or codes");
+  if (!w_pre && mode >= 0) value_error("codes need w_pre");
+  Tensor Rout, N, Q, S;
+  if (Y) Rout = create({T, H}, R.scalar_type(), R);
+  if (w_pre && values) N = create({T, H}, code == DG_IN_BF16 ? at::kBFloat16 : at::kFloat, R);
+  if (w_pre && mode >= 0) {
+    Q = create({T, H}, at::kByte, R);
+    S = create({T, (H + 127) / 128}, at::kFloat, R);
+  }
+  auto at_ = [](const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; };
+  const int st = lib.residual_norm(R.data_ptr(), r_code, Y ? Y->data_ptr() : nullptr, code, w_post, gate, kind, alpha,
+                                   w_pre, eps, at_(Rout), at_(N), at_(Q), static_cast<float*>(at_(S)),
+                                   mode < 0 ? DG_SCALE_POW2 : mode, T, H, stream());
+  if (st != DG_OK) return failure(st, "dg_residual_norm");
+  return tuple(Rout, N, Q, S);
+  END_HANDLE_TH_ERRORS
+}
+
+// residual_norm_bwd(dR, dN, R, Y, w_post, gate, alpha, w_pre, eps)
+PyObject* residual_norm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arguments(n, 9);
+  need(lib.residual_norm_bwd, "dg_residual_norm_bwd");
+  const Tensor *dR = optional(a[0], "dR"), *dN = optional(a[1], "dN"), *R = optional(a[2], "R"), *Y = optional(a[3], "Y");
+  const bool pre = a[7] != Py_None;
+  if (pre && (!R || !dN)) value_error("w_pre needs R and dN");
+  if (!pre && dN) value_error("dN needs w_pre");
+  if (!pre && !dR) value_error("there must be dR or dN");
+  if (!pre && !Y) value_error("without Y there must be w_pre");
+  const Tensor& like = pre ? *R : *dR;
+  const int r_code = check_values(like, pre ? "R" : "dR");
+  const int64_t T = like.size(0), H = like.size(1);
+  if (H < 1) return failure(DG_ERR_INVALID_ARG, "dg_residual_norm_bwd");
+  if (dR) check(*dR, "dR", {like.scalar_type()}, {T, H});
+  if (R) check(*R, "R", {like.scalar_type()}, {T, H});
+  if (dN) check(*dN, "dN", {at::kBFloat16, at::kFloat}, {T, H});
+  if (Y) check(*Y, "Y", {at::kBFloat16, at::kFloat}, {T, H});
+  if (Y && dN && Y->scalar_type() != dN->scalar_type()) value_error("Y and dN must have the same dtype");
+  const int code = dtype_code(dN ? *dN : *Y);
+  const float *w_post = weights_of(a[4], "w_post", {H}), *w_pre = weights_of(a[7], "w_pre", {H}), *gate;
+  const int kind = gate_of(a[5], T, H, &gate);
+  const float alpha = real(a[6], "alpha"), eps = real(a[8], "eps");
+  if (!Y && (w_post || kind != DG_GATE_NONE)) value_error("w_post and gate need Y");
+  const int64_t ws = lib.residual_norm_bwd_workspace(T, H, int(pre) + int(w_post || kind == DG_GATE_CHANNEL));
+  if (ws < 0) return failure(ws, "dg_residual_norm_bwd");
+  const Tensor dRout = create({T, H}, like.scalar_type(), like);
+  Tensor dY, dw_post, dgate, dw_pre, work;
+  if (Y) dY = create({T, H}, Y->scalar_type(), like);
+  if (w_post) dw_post = create({H}, at::kFloat, like);
+  if (kind != DG_GATE_NONE) dgate = create(optional(a[5], "gate")->sizes(), at::kFloat, like);
+  if (w_pre) dw_pre = create({H}, at::kFloat, like);
+  if (ws) work = create({ws}, at::kByte, like);
+  auto in = [](const Tensor* t) -> const void* { return t ? t->data_ptr() : nullptr; };
+  auto out = [](const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; };
+  const int st = lib.residual_norm_bwd(in(dR), in(dN), in(pre ? R : nullptr), r_code, in(Y), code, w_post, gate, kind,
+                                       alpha, w_pre, eps, out(dRout), out(dY), static_cast<float*>(out(dw_post)),
+                                       static_cast<float*>(out(dgate)), static_cast<float*>(out(dw_pre)), T, H,
+                                       out(work), stream());
+  if (st != DG_OK) return failure(st, "dg_residual_norm_bwd");
+  return tuple(dRout, dY, dw_post, dgate, dw_pre);
+  END_HANDLE_TH_ERRORS
+}
+
+// A list of gradients as the arrays that the library reads.
+struct Grads {
+  std::vector<const void*> at;
+  std::vector<int64_t> sizes;
+  std::vector<int> dtypes;
+  const Tensor* first = nullptr;
+
+  Grads(PyObject* list, const char* name) : items(list) {
+    if (!PyList_Check(list) && !PyTuple_Check(list)) type_error(std::string(name) + " must be a list of tensors");
+    const Py_ssize_t n = PySequence_Fast_GET_SIZE(items);
+    if (n > INT32_MAX) value_error("too many tensors");
+    at.reserve(n);
+    sizes.reserve(n);
+    dtypes.reserve(n);
+    for (Py_ssize_t i = 0; i < n; ++i) {
+      const Tensor& t = tensor(PySequence_Fast_GET_ITEM(items, i), name);
+      check(t, name, {at::kBFloat16, at::kFloat});
+      if (!first) first = &t;
+      at.push_back(t.data_ptr());
+      sizes.push_back(t.numel());
+      dtypes.push_back(dtype_code(t));
+    }
+  }
+  int count() const { return int(at.size()); }
+  const Tensor& operator[](int i) const { return THPVariable_Unpack(PySequence_Fast_GET_ITEM(items, i)); }
+
+ private:
+  PyObject* items;       // (the caller's, which holds its tensors)
+};
+
+// grad_norm(grads)
+PyObject* grad_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arguments(n, 1);
+  need(lib.grad_norm, "dg_grad_norm");
+  const Grads g(a[0], "grads");
+  if (!g.first) value_error("grads must not be empty");
+  const int64_t ws = lib.grad_norm_workspace(g.sizes.data(), g.dtypes.data(), g.count());
+  if (ws < 0) return failure(ws, "dg_grad_norm");
+  const Tensor norm = create({}, at::kFloat, *g.first);
+  const Tensor work = ws ? create({ws}, at::kByte, *g.first) : Tensor();
+  const int st = lib.grad_norm(g.at.data(), g.sizes.data(), g.dtypes.data(), g.count(), data<float>(norm),
+                               ws ? work.data_ptr() : nullptr, stream());
+  if (st != DG_OK) return failure(st, "dg_grad_norm");
+  return wrap(norm);
+  END_HANDLE_TH_ERRORS
+}
+
+// clip_grads(grads, norm, max_norm, out): the tensors written
+PyObject* clip_grads(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arguments(n, 4);
+  need(lib.clip_grads, "dg_clip_grads");
+  const Grads g(a[0], "grads");
+  const Tensor& norm = tensor(a[1], "norm");
+  const float* at = static_cast<const float*>(scalar(norm, "norm", at::kFloat));
+  const float max_norm = real(a[2], "max_norm");
+  PyObject* list = a[3] == Py_None ? a[0] : a[3];
+  const Grads out(list, "out");
+  if (out.count() != g.count())
+    value_error("out has " + std::to_string(out.count()) + " tensors, grads " + std::to_string(g.count()));
+  for (int i = 0; i < g.count(); ++i)
+    if (out[i].sizes() != g[i].sizes())
+      value_error("out has shape " + shape_of(out[i].sizes()) + ", expected " + shape_of(g[i].sizes()));
+  const int st = lib.clip_grads(g.at.data(), g.sizes.data(), g.dtypes.data(), g.count(), at, max_norm,
+                                const_cast<void* const*>(out.at.data()), out.dtypes.data(), stream());
+  if (st != DG_OK) return failure(st, "dg_clip_grads");
+  for (int i = 0; i < out.count(); ++i)
+    if (!out[i].is_inference()) out[i].unsafeGetTensorImpl()->bump_version();
+  Py_INCREF(list);
+  return list;
+  END_HANDLE_TH_ERRORS
+}
+
 // load(path of libdg.so, DGError)
 PyObject* load(PyObject*, PyObject* args) {
   const char* path;
@@ -406,6 +701,15 @@ PyObject* load(PyObject*, PyObject* args) {
     PyErr_Format(PyExc_RuntimeError, "%s lacks functions of dg.h: build it again", path);
     return nullptr;
   }
+  find(lib.moe_route_workspace, "dg_moe_route_workspace");
+  find(lib.moe_route, "dg_moe_route");
+  find(lib.moe_route_bwd, "dg_moe_route_bwd");
+  find(lib.residual_norm, "dg_residual_norm");
+  find(lib.residual_norm_bwd_workspace, "dg_residual_norm_bwd_workspace");
+  find(lib.residual_norm_bwd, "dg_residual_norm_bwd");
+  find(lib.grad_norm_workspace, "dg_grad_norm_workspace");
+  find(lib.grad_norm, "dg_grad_norm");
+  find(lib.clip_grads, "dg_clip_grads");
   Py_INCREF(error);
   Py_XDECREF(dg_error);
   dg_error = error;
@@ -422,6 +726,12 @@ PyMethodDef methods[] = {{"load", load, METH_VARARGS, nullptr},
                          DG_FAST(swiglu_fp8),
                          DG_FAST(swiglu_fp8_bwd),
                          DG_FAST(grouped_wgrad_fp8),
+                         DG_FAST(moe_route),
+                         DG_FAST(moe_route_bwd),
+                         DG_FAST(residual_norm),
+                         DG_FAST(residual_norm_bwd),
+                         DG_FAST(grad_norm),
+                         DG_FAST(clip_grads),
                          {nullptr, nullptr, 0, nullptr}};
 #undef DG_FAST
 

@@ -1,0 +1,394 @@
+// Host side of the operators that make the mixture-of-experts layer a block of a
+// model: the router, the norms around the block, and gradient clipping.  Argument
+// checks (before any HIP call), launch shapes, and the kernels.
+#include <hip/hip_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <memory>
+#include <new>
+#include <type_traits>
+
+#include "clip.hpp"
+#include "dg.h"
+#include "host.hpp"
+#include "norm.hpp"
+#include "route.hpp"
+
+namespace dg {
+
+#define DG_BLOCK_KERNEL(NAME, THREADS, ARGS, ...) \
+  __global__ __launch_bounds__(THREADS) void NAME(ARGS p) { __VA_ARGS__(p); }
+#define DG_ROUTE_KERNELS(T, BF16)                                                                      \
+  DG_BLOCK_KERNEL(dg_moe_route_##T##_16x4, kRouteThreads, RouteArgs, route_body<BF16, 16, 4, false>)          \
+  DG_BLOCK_KERNEL(dg_moe_route_##T##_16x16, kRouteThreads, RouteArgs, route_body<BF16, 16, 16, false>)        \
+  DG_BLOCK_KERNEL(dg_moe_route_##T##_64x4, kRouteThreads, RouteArgs, route_body<BF16, 64, 4, false>)          \
+  DG_BLOCK_KERNEL(dg_moe_route_##T##_64x16, kRouteThreads, RouteArgs, route_body<BF16, 64, 16, false>)        \
+  DG_BLOCK_KERNEL(dg_moe_route_##T##_16x4_bias, kRouteThreads, RouteArgs, route_body<BF16, 16, 4, true>)      \
+  DG_BLOCK_KERNEL(dg_moe_route_##T##_16x16_bias, kRouteThreads, RouteArgs, route_body<BF16, 16, 16, true>)    \
+  DG_BLOCK_KERNEL(dg_moe_route_##T##_64x4_bias, kRouteThreads, RouteArgs, route_body<BF16, 64, 4, true>)      \
+  DG_BLOCK_KERNEL(dg_moe_route_##T##_64x16_bias, kRouteThreads, RouteArgs, route_body<BF16, 64, 16, true>)    \
+  DG_BLOCK_KERNEL(dg_moe_route_bwd_##T##_16x4, kRouteBwdThreads, RouteBwdArgs, route_bwd_body<BF16, 16, 4>)   \
+  DG_BLOCK_KERNEL(dg_moe_route_bwd_##T##_16x16, kRouteBwdThreads, RouteBwdArgs, route_bwd_body<BF16, 16, 16>) \
+  DG_BLOCK_KERNEL(dg_moe_route_bwd_##T##_64x4, kRouteBwdThreads, RouteBwdArgs, route_bwd_body<BF16, 64, 4>)   \
+  DG_BLOCK_KERNEL(dg_moe_route_bwd_##T##_64x16, kRouteBwdThreads, RouteBwdArgs, route_bwd_body<BF16, 64, 16>)
+DG_ROUTE_KERNELS(bf16, true)
+DG_ROUTE_KERNELS(f32, false)
+DG_BLOCK_KERNEL(dg_moe_route_finish, kRouteThreads, RouteArgs, route_finish)
+#undef DG_ROUTE_KERNELS
+
+// (templates: stream and value types, codes, whole rows, wide rows)
+template <bool RB, bool YB, int CODES, bool WHOLE, bool WIDE>
+DG_BLOCK_KERNEL(dg_residual_norm_kernel, kNormMaxThreads, NormArgs, norm_body<RB, YB, CODES, WHOLE, WIDE>)
+template <bool RB, bool YB, bool WHOLE, bool WIDE>
+DG_BLOCK_KERNEL(dg_residual_norm_bwd_kernel, kNormMaxThreads, NormBwdArgs, norm_bwd_body<RB, YB, WHOLE, WIDE>)
+DG_BLOCK_KERNEL(dg_residual_norm_columns, 1024, NormColumnsArgs, norm_columns_body)
+
+DG_BLOCK_KERNEL(dg_grad_squares, kClipThreads, ClipBatch, clip_squares_body)
+DG_BLOCK_KERNEL(dg_grad_norm_sum, kClipNormThreads, ClipNormArgs, clip_norm_body)
+DG_BLOCK_KERNEL(dg_clip_scale, kClipThreads, ClipBatch, clip_scale_body)
+#undef DG_BLOCK_KERNEL
+
+}  // namespace dg
+
+namespace {
+
+using namespace dg_host;
+
+// ---- router ------------------------------------------------------------------------
+
+int check_route(int64_t T, int64_t E, int top_k) {
+  if (T < 0 || E < 1 || top_k < 1 || T > kMaxDim || E > kMaxDim || top_k > E || T * top_k > kMaxDim)
+    return DG_ERR_INVALID_ARG;
+  if (E > dg::kRouteMaxExperts || top_k > 64 || T * top_k > kMaxSlots) return DG_ERR_UNSUPPORTED;
+  return DG_OK;
+}
+
+// Lanes and logits per lane: a row of 16 lanes holds up to 256 experts and 16 choices.
+int route_lanes(int64_t E, int top_k) { return E <= 256 && top_k <= 16 ? 16 : 64; }
+int route_variant(int64_t E, int top_k) {
+  if (route_lanes(E, top_k) == 16) return E <= 64 ? 0 : 1;
+  return E <= 256 ? 2 : 3;
+}
+
+int64_t route_blocks(int64_t T, int64_t E, int top_k, bool balance) {
+  const int64_t per = dg::kRouteThreads / route_lanes(E, top_k);
+  return std::min<int64_t>(std::max<int64_t>(1, ceil_div(T, per)), balance ? dg::kRouteMaxBlocks : 65536);
+}
+
+bool valid_scores(int score, int renormalise, float scale) {
+  return (score == DG_SCORE_SOFTMAX || score == DG_SCORE_SIGMOID) && (renormalise == 0 || renormalise == 1) &&
+         isfinite(scale);
+}
+
+// ---- norms -------------------------------------------------------------------------
+
+int norm_threads(int64_t H) {
+  return int(std::min<int64_t>(ceil_div(ceil_div(H, dg::kNormColumns), 64) * 64, dg::kNormMaxThreads));
+}
+
+int64_t norm_bwd_blocks(int64_t T, int64_t H) {
+  // (partial sums of 16 MB at most for wide rows)
+  const int64_t most = H <= dg::kNormRegisterWidth ? 512 : std::max<int64_t>(1, (int64_t(1) << 22) / H);
+  return std::min(T, std::min<int64_t>(most, 512));
+}
+
+int check_norm(int r_dtype, int dtype, const void* Y, const float* w_post, const float* gate, int gate_kind,
+               float alpha, const float* w_pre, float eps, int64_t T, int64_t H) {
+  if (!valid_type(r_dtype) || !valid_type(dtype)) return DG_ERR_INVALID_ARG;
+  if (gate_kind != DG_GATE_NONE && gate_kind != DG_GATE_CHANNEL && gate_kind != DG_GATE_TOKEN) return DG_ERR_INVALID_ARG;
+  if (!isfinite(alpha) || !isfinite(eps) || !(eps > 0.f)) return DG_ERR_INVALID_ARG;
+  if (T < 0 || H < 1 || T > kMaxDim || H > kMaxDim) return DG_ERR_INVALID_ARG;
+  // (what has no rows may have no address)
+  if (T > 0 && Y == nullptr && (w_post || gate || gate_kind != DG_GATE_NONE || !w_pre)) return DG_ERR_INVALID_ARG;
+  if ((gate == nullptr) != (gate_kind == DG_GATE_NONE) && !(T == 0 && gate_kind == DG_GATE_TOKEN)) return DG_ERR_INVALID_ARG;
+  if (!aligned(Y, 16) || !aligned(w_post, 16) || !aligned(gate, gate_kind == DG_GATE_TOKEN ? 4 : 16) ||
+      !aligned(w_pre, 16))
+    return DG_ERR_INVALID_ARG;
+  return DG_OK;
+}
+
+template <bool RB, bool YB, int CODES>
+void (*norm_kernel(bool whole, bool wide))(dg::NormArgs) {
+  if constexpr (CODES != dg::kCodesNone) {
+    return wide ? dg::dg_residual_norm_kernel<RB, YB, CODES, true, true>
+                : dg::dg_residual_norm_kernel<RB, YB, CODES, true, false>;
+  } else {
+    return whole ? (wide ? dg::dg_residual_norm_kernel<RB, YB, CODES, true, true>
+                         : dg::dg_residual_norm_kernel<RB, YB, CODES, true, false>)
+                 : (wide ? dg::dg_residual_norm_kernel<RB, YB, CODES, false, true>
+                         : dg::dg_residual_norm_kernel<RB, YB, CODES, false, false>);
+  }
+}
+
+template <bool RB, bool YB>
+void (*norm_kernel(int codes, bool whole, bool wide))(dg::NormArgs) {
+  return codes == dg::kCodesNone   ? norm_kernel<RB, YB, dg::kCodesNone>(whole, wide)
+         : codes == dg::kCodesPow2 ? norm_kernel<RB, YB, dg::kCodesPow2>(whole, wide)
+                                   : norm_kernel<RB, YB, dg::kCodesAmax>(whole, wide);
+}
+
+template <bool RB, bool YB>
+void (*norm_bwd_kernel(bool whole, bool wide))(dg::NormBwdArgs) {
+  return whole ? (wide ? dg::dg_residual_norm_bwd_kernel<RB, YB, true, true>
+                       : dg::dg_residual_norm_bwd_kernel<RB, YB, true, false>)
+               : (wide ? dg::dg_residual_norm_bwd_kernel<RB, YB, false, true>
+                       : dg::dg_residual_norm_bwd_kernel<RB, YB, false, false>);
+}
+
+// ---- clipping ------------------------------------------------------------------------
+
+int elem(int dtype) { return dtype == DG_IN_BF16 ? 2 : 4; }
+
+// Sizes and types of a list of tensors; its chunks, or a negative status.
+int64_t clip_chunks(const int64_t* sizes, const int* dtypes, int count) {
+  if (count < 0 || (count > 0 && (sizes == nullptr || dtypes == nullptr))) return DG_ERR_INVALID_ARG;
+  int64_t chunks = 0;
+  for (int i = 0; i < count; ++i) {
+    if (sizes[i] < 0 || sizes[i] > (int64_t(1) << 45) || !valid_type(dtypes[i])) return DG_ERR_INVALID_ARG;
+    chunks += ceil_div(sizes[i], dg::kClipChunk);
+    if (chunks > kMaxDim) return DG_ERR_UNSUPPORTED;
+  }
+  return chunks;
+}
+
+// Whether what the outputs' addresses cover is written once, and read by no other
+// tensor's: ranges in order of their addresses, grads[i] itself counting for outs[i].
+// -1: no memory to sort them in.
+int clip_disjoint(const void* const* grads, const int64_t* sizes, const int* dtypes, int count, void* const* outs,
+                  const int* out_dtypes) {
+  struct Range {
+    uintptr_t begin, end;
+    bool out;
+  };
+  std::unique_ptr<Range[]> r(new (std::nothrow) Range[2 * size_t(count)]);
+  if (!r) return -1;
+  size_t n = 0;
+  bool sorted = true;
+  auto add = [&](const void* p, int64_t bytes, bool out) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    r[n] = Range{a, a + uintptr_t(bytes), out};
+    sorted = sorted && (n == 0 || r[n - 1].begin <= a);
+    ++n;
+  };
+  for (int i = 0; i < count; ++i) {
+    if (sizes[i] == 0) continue;
+    if (grads[i] != outs[i]) add(grads[i], sizes[i] * elem(dtypes[i]), false);
+    add(outs[i], sizes[i] * elem(out_dtypes[i]), true);
+  }
+  if (!sorted) std::sort(r.get(), r.get() + n, [](const Range& a, const Range& b) { return a.begin < b.begin; });
+  uintptr_t any = 0, out = 0;                       // ends of the ranges so far, and of the outputs among them
+  for (size_t i = 0; i < n; ++i) {
+    if (r[i].begin < (r[i].out ? any : out)) return 0;
+    any = std::max(any, r[i].end);
+    if (r[i].out) out = std::max(out, r[i].end);
+  }
+  return 1;
+}
+
+// The launches of a kernel over a list, up to kClipTensors tensors that are not empty
+// each; `fill` completes a tensor's entry.
+template <typename F>
+int clip_launches(void (*kernel)(dg::ClipBatch), dg::ClipBatch& b, const void* const* grads, const int64_t* sizes,
+                  const int* dtypes, int count, hipStream_t stream, F fill) {
+  b.count = b.chunks = 0;
+  for (int i = 0; i <= count; ++i) {
+    const int64_t chunks = i < count ? ceil_div(sizes[i], dg::kClipChunk) : 0;
+    if (b.count == dg::kClipTensors || (i == count && b.count > 0)) {
+      const int st = launch(kernel, b, b.chunks, dg::kClipThreads, stream);
+      if (st != DG_OK) return st;
+      if (b.part) b.part += b.chunks;
+      b.count = b.chunks = 0;
+    }
+    if (chunks == 0) continue;
+    dg::ClipTensor& t = b.t[b.count++];
+    t = dg::ClipTensor{grads[i], nullptr, sizes[i], b.chunks, uint8_t(dtypes[i] == DG_IN_BF16), 0,
+                       uint8_t(aligned(grads[i], 16)), 0};
+    fill(t, i);
+    b.chunks += int(chunks);
+  }
+  return DG_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t dg_moe_route_workspace(int64_t T, int64_t E, int top_k) {
+  const int st = check_route(T, E, top_k);
+  if (st != DG_OK) return st;
+  return route_blocks(T, E, top_k, true) * (8 * E + 4);
+}
+
+int dg_moe_route(const void* logits, int dtype, const float* bias, const uint8_t* mask, int64_t T, int64_t E, int top_k,
+                 int score, int renormalise, float scale, int32_t* ids, float* weights, int32_t* counts,
+                 float* prob_sums, int32_t* routed, float* loss, void* workspace, hipStream_t stream) {
+  if (!valid_type(dtype) || !valid_scores(score, renormalise, scale)) return DG_ERR_INVALID_ARG;
+  const int st = check_route(T, E, top_k);
+  if (st != DG_OK) return st;
+  const bool balance = counts != nullptr;
+  if ((prob_sums != nullptr) != balance || (routed != nullptr) != balance || (loss != nullptr) != balance)
+    return DG_ERR_INVALID_ARG;
+  if (!aligned(counts, 4) || !aligned(prob_sums, 4) || !aligned(routed, 4) || !aligned(loss, 4) || !aligned(bias, 4))
+    return DG_ERR_INVALID_ARG;
+  if (balance && bad(workspace, 4)) return DG_ERR_INVALID_ARG;
+  if (T > 0 && (bad(logits, 16) || bad(ids, 4) || bad(weights, 4))) return DG_ERR_INVALID_ARG;
+  if (T == 0 && !balance) return DG_OK;
+  const int64_t nb = route_blocks(T, E, top_k, balance);
+  float* part = static_cast<float*>(workspace);
+  int32_t* ints = reinterpret_cast<int32_t*>(part) + nb * E;
+  dg::RouteArgs a{logits, bias, mask, ids, weights, counts, prob_sums, routed, loss, part, ints, ints + nb * E,
+                  int(T), int(E), top_k, int(nb), score == DG_SCORE_SIGMOID, renormalise, scale};
+#define DG_ROUTE_TABLE(T)                                                                                       \
+  {{dg::dg_moe_route_##T##_16x4, dg::dg_moe_route_##T##_16x16, dg::dg_moe_route_##T##_64x4,                     \
+    dg::dg_moe_route_##T##_64x16},                                                                              \
+   {dg::dg_moe_route_##T##_16x4_bias, dg::dg_moe_route_##T##_16x16_bias, dg::dg_moe_route_##T##_64x4_bias,      \
+    dg::dg_moe_route_##T##_64x16_bias}}
+  static void (*const kernels[2][2][4])(dg::RouteArgs) = {DG_ROUTE_TABLE(f32), DG_ROUTE_TABLE(bf16)};
+#undef DG_ROUTE_TABLE
+  const int st1 = launch(kernels[dtype == DG_IN_BF16][bias != nullptr][route_variant(E, top_k)], a, nb,
+                         dg::kRouteThreads, stream);
+  if (st1 != DG_OK || !balance) return st1;
+  return launch(dg::dg_moe_route_finish, a, 1, dg::kRouteThreads, stream);
+}
+
+int dg_moe_route_bwd(const float* dweights, const void* logits, int dtype, const int32_t* ids, const int32_t* counts,
+                     const int32_t* routed, const float* dloss, int64_t T, int64_t E, int top_k, int score,
+                     int renormalise, float scale, void* dlogits, hipStream_t stream) {
+  if (!valid_type(dtype) || !valid_scores(score, renormalise, scale)) return DG_ERR_INVALID_ARG;
+  const int st = check_route(T, E, top_k);
+  if (st != DG_OK) return st;
+  if ((routed != nullptr) != (counts != nullptr) || (dloss != nullptr) != (counts != nullptr)) return DG_ERR_INVALID_ARG;
+  if (!aligned(counts, 4) || !aligned(routed, 4) || !aligned(dloss, 4)) return DG_ERR_INVALID_ARG;
+  if (T == 0) return DG_OK;
+  if (bad(dweights, 4) || bad(logits, 16) || bad(ids, 4) || bad(dlogits, 16)) return DG_ERR_INVALID_ARG;
+  dg::RouteBwdArgs a{logits, ids, dweights, counts, routed, dloss, dlogits, int(T), int(E), top_k,
+                     score == DG_SCORE_SIGMOID, renormalise, scale};
+#define DG_ROUTE_TABLE(T)                                                                                       \
+  {dg::dg_moe_route_bwd_##T##_16x4, dg::dg_moe_route_bwd_##T##_16x16, dg::dg_moe_route_bwd_##T##_64x4,          \
+   dg::dg_moe_route_bwd_##T##_64x16}
+  static void (*const kernels[2][4])(dg::RouteBwdArgs) = {DG_ROUTE_TABLE(f32), DG_ROUTE_TABLE(bf16)};
+#undef DG_ROUTE_TABLE
+  return launch(kernels[dtype == DG_IN_BF16][route_variant(E, top_k)], a,
+                ceil_div(T, dg::kRouteBwdThreads / route_lanes(E, top_k)), dg::kRouteBwdThreads, stream);
+}
+
+int dg_residual_norm(const void* R, int r_dtype, const void* Y, int dtype, const float* w_post, const float* gate,
+                     int gate_kind, float alpha, const float* w_pre, float eps, void* R_out, void* N, void* Q, float* S,
+                     int scale_mode, int64_t T, int64_t H, hipStream_t stream) {
+  const int st = check_norm(r_dtype, dtype, Y, w_post, gate, gate_kind, alpha, w_pre, eps, T, H);
+  if (st != DG_OK) return st;
+  if (scale_mode != DG_SCALE_AMAX && scale_mode != DG_SCALE_POW2) return DG_ERR_INVALID_ARG;
+  if ((Q == nullptr) != (S == nullptr)) return DG_ERR_INVALID_ARG;
+  if (T == 0) return DG_OK;
+  if (bad(R, 16) || !aligned(R_out, 16) || !aligned(N, 16) || !aligned(Q, 16) || !aligned(S, 4))
+    return DG_ERR_INVALID_ARG;
+  if ((R_out != nullptr) != (Y != nullptr) || (N != nullptr || Q != nullptr) != (w_pre != nullptr))
+    return DG_ERR_INVALID_ARG;
+  if (R_out && (R_out == R || R_out == Y)) return DG_ERR_INVALID_ARG;
+  if (N && (N == R || N == Y)) return DG_ERR_INVALID_ARG;
+  if (H > kMaxWidth || (Q && H % 16 != 0)) return DG_ERR_UNSUPPORTED;
+  const bool wide = H > dg::kNormRegisterWidth, whole = H % 8 == 0;
+  const int threads = norm_threads(H);
+  dg::NormArgs a{R, Y, w_post, gate, w_pre, R_out, N, static_cast<uint8_t*>(Q), S, eps, alpha, int(T), int(H),
+                 int(ceil_div(H, 128)), gate_kind};
+  const int codes = !Q ? dg::kCodesNone : scale_mode == DG_SCALE_POW2 ? dg::kCodesPow2 : dg::kCodesAmax;
+  const bool rb = r_dtype == DG_IN_BF16, yb = dtype == DG_IN_BF16;
+  const auto kernel = rb ? (yb ? norm_kernel<true, true>(codes, whole, wide) : norm_kernel<true, false>(codes, whole, wide))
+                         : (yb ? norm_kernel<false, true>(codes, whole, wide) : norm_kernel<false, false>(codes, whole, wide));
+  return launch(kernel, a, std::min<int64_t>(T, 256 * (2048 / threads)), threads, stream);
+}
+
+int64_t dg_residual_norm_bwd_workspace(int64_t T, int64_t H, int sums) {
+  if (T < 0 || H < 1 || T > kMaxDim || H > kMaxDim || sums < 0 || sums > 2) return DG_ERR_INVALID_ARG;
+  if (H > kMaxWidth) return DG_ERR_UNSUPPORTED;
+  return 4 * norm_bwd_blocks(T, H) * H * sums;
+}
+
+int dg_residual_norm_bwd(const void* dR, const void* dN, const void* R, int r_dtype, const void* Y, int dtype,
+                         const float* w_post, const float* gate, int gate_kind, float alpha, const float* w_pre,
+                         float eps, void* dR_out, void* dY, float* dw_post, float* dgate, float* dw_pre, int64_t T,
+                         int64_t H, void* workspace, hipStream_t stream) {
+  const int st = check_norm(r_dtype, dtype, Y, w_post, gate, gate_kind, alpha, w_pre, eps, T, H);
+  if (st != DG_OK) return st;
+  const bool token = gate_kind == DG_GATE_TOKEN, channel = gate_kind == DG_GATE_CHANNEL;
+  if (H > kMaxWidth) return DG_ERR_UNSUPPORTED;
+  if ((w_pre && bad(dw_pre, 4)) || (w_post && bad(dw_post, 4)) || (channel && bad(dgate, 4))) return DG_ERR_INVALID_ARG;
+  if ((!w_pre && dw_pre) || (!w_post && dw_post) || (gate_kind == DG_GATE_NONE && dgate)) return DG_ERR_INVALID_ARG;
+  const bool pre = w_pre != nullptr, post = w_post != nullptr || channel;
+  const int64_t nb = norm_bwd_blocks(T, H);
+  float* part = static_cast<float*>(workspace);
+  float* part_pre = pre ? part : nullptr;
+  float* part_post = post ? part + (pre ? nb * H : 0) : nullptr;
+  if (T > 0) {
+    if (bad(dR_out, 16) || !aligned(dR, 16) || (token && bad(dgate, 4))) return DG_ERR_INVALID_ARG;
+    if (pre ? bad(R, 16) || bad(dN, 16) : dN != nullptr || dR == nullptr) return DG_ERR_INVALID_ARG;
+    if ((dY != nullptr) != (Y != nullptr) || !aligned(dY, 16)) return DG_ERR_INVALID_ARG;
+    if (dR_out == dR || dR_out == R || dR_out == dN || dR_out == Y || dR_out == dY) return DG_ERR_INVALID_ARG;
+    if (dY && (dY == Y || dY == R || dY == dR || dY == dN)) return DG_ERR_INVALID_ARG;
+    if ((pre || post) && bad(workspace, 16)) return DG_ERR_INVALID_ARG;
+    const bool wide = H > dg::kNormRegisterWidth, whole = H % 8 == 0;
+    dg::NormBwdArgs a{dR, dN, pre ? R : nullptr, Y, w_post, gate, w_pre, dR_out, dY, token ? dgate : nullptr,
+                      part_pre, part_post, eps, alpha, int(T), int(H), gate_kind};
+    const bool rb = r_dtype == DG_IN_BF16, yb = dtype == DG_IN_BF16;
+    const auto kernel = rb ? (yb ? norm_bwd_kernel<true, true>(whole, wide) : norm_bwd_kernel<true, false>(whole, wide))
+                           : (yb ? norm_bwd_kernel<false, true>(whole, wide) : norm_bwd_kernel<false, false>(whole, wide));
+    const int st1 = launch(kernel, a, nb, norm_threads(H), stream);
+    if (st1 != DG_OK) return st1;
+  }
+  if (!pre && !post) return DG_OK;
+  // (without rows the sums are zeros)
+  const int blocks = int(ceil_div(H, 32));
+  dg::NormColumnsArgs c{part_pre, part_post, w_post, channel ? gate : nullptr, dw_pre, dw_post, channel ? dgate : nullptr,
+                        int(nb), int(H), pre ? blocks : 0};
+  return launch(dg::dg_residual_norm_columns, c, blocks * (pre + post), 1024, stream);
+}
+
+int64_t dg_grad_norm_workspace(const int64_t* sizes, const int* dtypes, int count) {
+  const int64_t chunks = clip_chunks(sizes, dtypes, count);
+  return chunks < 0 ? chunks : 8 * chunks;
+}
+
+int dg_grad_norm(const void* const* grads, const int64_t* sizes, const int* dtypes, int count, float* norm,
+                 void* workspace, hipStream_t stream) {
+  const int64_t chunks = clip_chunks(sizes, dtypes, count);
+  if (chunks < 0) return int(chunks);
+  if (bad(norm, 4) || (chunks > 0 && (grads == nullptr || bad(workspace, 8)))) return DG_ERR_INVALID_ARG;
+  for (int i = 0; i < count; ++i)
+    if (sizes[i] > 0 && bad(grads[i], elem(dtypes[i]))) return DG_ERR_INVALID_ARG;
+  dg::ClipBatch b{};
+  b.part = static_cast<double*>(workspace);
+  const int st = clip_launches(dg::dg_grad_squares, b, grads, sizes, dtypes, count, stream, [](dg::ClipTensor&, int) {});
+  if (st != DG_OK) return st;
+  dg::ClipNormArgs a{static_cast<const double*>(workspace), chunks, norm};
+  return launch(dg::dg_grad_norm_sum, a, 1, dg::kClipNormThreads, stream);
+}
+
+int dg_clip_grads(const void* const* grads, const int64_t* sizes, const int* dtypes, int count, const float* norm,
+                  float max_norm, void* const* outs, const int* out_dtypes, hipStream_t stream) {
+  const int64_t chunks = clip_chunks(sizes, dtypes, count);
+  if (chunks < 0) return int(chunks);
+  if (bad(norm, 4) || !isfinite(max_norm) || !(max_norm > 0.f)) return DG_ERR_INVALID_ARG;
+  if (chunks == 0) return DG_OK;
+  if (grads == nullptr || outs == nullptr || out_dtypes == nullptr) return DG_ERR_INVALID_ARG;
+  for (int i = 0; i < count; ++i) {
+    if (!valid_type(out_dtypes[i])) return DG_ERR_INVALID_ARG;
+    if (sizes[i] == 0) continue;
+    if (bad(grads[i], elem(dtypes[i])) || bad(outs[i], elem(out_dtypes[i]))) return DG_ERR_INVALID_ARG;
+    // in place the types are the same
+    if (grads[i] == outs[i] && dtypes[i] != out_dtypes[i]) return DG_ERR_INVALID_ARG;
+  }
+  const int disjoint = clip_disjoint(grads, sizes, dtypes, count, outs, out_dtypes);
+  if (disjoint <= 0) return disjoint == 0 ? DG_ERR_INVALID_ARG : DG_ERR_LAUNCH;
+  dg::ClipBatch b{};
+  b.norm = norm;
+  b.max_norm = max_norm;
+  return clip_launches(dg::dg_clip_scale, b, grads, sizes, dtypes, count, stream, [&](dg::ClipTensor& t, int i) {
+    t.out = outs[i];
+    t.out_bf16 = out_dtypes[i] == DG_IN_BF16;
+    t.whole = t.whole && aligned(outs[i], 16);
+  });
+}
+
+}  // extern "C"

@@ -1,0 +1,156 @@
+// The global norm of many gradients, and their clipping, gfx950.
+//
+//   norm = sqrt(sum over all tensors of g^2);   out = g min(1, max_norm / norm)
+//
+// The tensors' addresses and sizes are arguments of the launch itself (up to
+// kClipTensors a launch), so that nothing has to be laid out on the device first and a
+// captured graph holds them.  Work is cut into chunks of kClipChunk elements, a
+// workgroup each; a chunk finds its tensor by a binary search over the tensors' first
+// chunks.  Squares are summed in 64 bits (FP32's largest gradients then do not
+// overflow), the chunks' sums in their order: nothing is atomic.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "common.hpp"
+#include "groups.hpp"
+#include "moe.hpp"
+
+namespace dg {
+
+constexpr int kClipTensors = 96;
+constexpr int kClipThreads = 256;
+constexpr int kClipChunk = 16384;
+
+struct ClipTensor {
+  const void* g;
+  void* out;                 // clipping only
+  int64_t n;
+  int32_t first;             // first chunk
+  uint8_t bf16, out_bf16, whole, pad;   // whole: 16-byte aligned
+};
+
+struct ClipBatch {
+  ClipTensor t[kClipTensors];
+  int count, chunks;
+  double* part;              // [chunks], this launch's
+  const float* norm;
+  float max_norm;
+};
+static_assert(sizeof(ClipBatch) <= 4096, "arguments of a launch");
+
+__device__ __forceinline__ int clip_tensor(const ClipBatch& p, int chunk) {
+  int lo = 0, hi = p.count - 1;                 // the last tensor whose first chunk is not past this one
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (p.t[mid].first <= chunk) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+template <bool BF16>
+__device__ __forceinline__ double chunk_squares(const ClipTensor& x, int64_t begin, int n) {
+  constexpr int V = BF16 ? 8 : 4;
+  double sum = 0.0;
+  int done = 0;
+  if (x.whole) {
+    done = n / V * V;
+    for (int i = threadIdx.x * V; i < done; i += kClipThreads * V) {
+      float v[V];
+      load_values<BF16, V>(x.g, size_t(begin) + i, v);
+#pragma unroll
+      for (int k = 0; k < V; ++k) sum += double(v[k]) * v[k];
+    }
+  }
+  for (int i = done + threadIdx.x; i < n; i += kClipThreads) {
+    float v;
+    load_values<BF16, 1>(x.g, size_t(begin) + i, &v);
+    sum += double(v) * v;
+  }
+  return sum;
+}
+
+__device__ __forceinline__ void clip_squares_body(const ClipBatch& p) {
+  __shared__ double sums[kClipThreads / 64];
+  const int chunk = block_index();
+  if (chunk >= p.chunks) return;
+  const ClipTensor& x = p.t[clip_tensor(p, chunk)];
+  const int64_t begin = int64_t(chunk - x.first) * kClipChunk;
+  const int n = int(min(x.n - begin, int64_t(kClipChunk)));
+  double s = x.bf16 ? chunk_squares<true>(x, begin, n) : chunk_squares<false>(x, begin, n);
+  s = group_sum<64>(s);
+  if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) p.part[chunk] = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+}
+
+struct ClipNormArgs {
+  const double* part;        // [n]
+  int64_t n;
+  float* norm;
+};
+
+constexpr int kClipNormThreads = 1024;
+
+__device__ __forceinline__ void clip_norm_body(const ClipNormArgs& p) {
+  __shared__ double sums[kClipNormThreads / 64];
+  double s = 0.0;
+  for (int64_t i = threadIdx.x; i < p.n; i += kClipNormThreads) s += p.part[i];
+  s = group_sum<64>(s);
+  if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < kClipNormThreads / 64; ++w) s += sums[w];
+    *p.norm = float(sqrt(s));
+  }
+}
+
+template <bool IN, bool OUT>
+__device__ __forceinline__ void chunk_scaled(const ClipTensor& x, int64_t begin, int n, float f) {
+  int done = 0;
+  if (x.whole) {
+    done = n / 8 * 8;
+    for (int i = threadIdx.x * 8; i < done; i += kClipThreads * 8) {
+      float v[8];
+      load_values<IN, IN ? 8 : 4>(x.g, size_t(begin) + i, v);
+      if constexpr (!IN) load_values<IN, 4>(x.g, size_t(begin) + i + 4, v + 4);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] *= f;
+      store_values<OUT, OUT ? 8 : 4>(x.out, size_t(begin) + i, v);
+      if constexpr (!OUT) store_values<OUT, 4>(x.out, size_t(begin) + i + 4, v + 4);
+    }
+  }
+  for (int i = done + threadIdx.x; i < n; i += kClipThreads) {
+    float v;
+    load_values<IN, 1>(x.g, size_t(begin) + i, &v);
+    v *= f;
+    store_values<OUT, 1>(x.out, size_t(begin) + i, &v);
+  }
+}
+
+// NaN as the norm makes every gradient NaN; an infinite one makes them 0 (and
+// infinite gradients NaN), as the formula does.
+__device__ __forceinline__ float clip_factor(float norm, float max_norm) {
+  const double f = double(max_norm) / double(norm);
+  return f >= 1.0 ? 1.f : float(f);
+}
+
+__device__ __forceinline__ void clip_scale_body(const ClipBatch& p) {
+  const int chunk = block_index();
+  if (chunk >= p.chunks) return;
+  const float f = clip_factor(*p.norm, p.max_norm);
+  const ClipTensor& x = p.t[clip_tensor(p, chunk)];
+  if (f == 1.f && x.g == x.out) return;         // in place, and nothing to change
+  const int64_t begin = int64_t(chunk - x.first) * kClipChunk;
+  const int n = int(min(x.n - begin, int64_t(kClipChunk)));
+  if (x.bf16) {
+    if (x.out_bf16) chunk_scaled<true, true>(x, begin, n, f);
+    else chunk_scaled<true, false>(x, begin, n, f);
+  } else {
+    if (x.out_bf16) chunk_scaled<false, true>(x, begin, n, f);
+    else chunk_scaled<false, false>(x, begin, n, f);
+  }
+}
+
+}  // namespace dg

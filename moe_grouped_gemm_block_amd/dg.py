@@ -29,6 +29,11 @@ DG_IDX_I32 = 0
 DG_IDX_I64 = 1
 DG_SCALE_AMAX = 0
 DG_SCALE_POW2 = 1
+DG_SCORE_SOFTMAX = 0
+DG_SCORE_SIGMOID = 1
+DG_GATE_NONE = 0
+DG_GATE_CHANNEL = 1
+DG_GATE_TOKEN = 2
 DG_OK = 0
 DG_ERR_INVALID_ARG = -1
 DG_ERR_UNSUPPORTED = -2
@@ -38,7 +43,9 @@ EXPORTED = ("dg_gemm_fp8_blockscaled", "dg_grouped_gemm_fp8", "dg_gemm_fp8_ex", 
             "dg_grouped_gemm_fp8_ex", "dg_grouped_gemm_fp8_ex_counts", "dg_grouped_gemm_fp8_segments",
             "dg_quantize_fp8_blockscaled", "dg_moe_sort", "dg_moe_rows", "dg_moe_sort_workspace",
             "dg_moe_permute", "dg_moe_permute_fp8", "dg_moe_combine", "dg_moe_combine_bwd", "dg_swiglu_fp8",
-            "dg_swiglu_fp8_bwd", "dg_grouped_wgrad_fp8", "dg_status_string")
+            "dg_swiglu_fp8_bwd", "dg_grouped_wgrad_fp8", "dg_moe_route", "dg_moe_route_workspace", "dg_moe_route_bwd",
+            "dg_residual_norm", "dg_residual_norm_bwd", "dg_residual_norm_bwd_workspace", "dg_grad_norm",
+            "dg_grad_norm_workspace", "dg_clip_grads", "dg_status_string")
 
 _lib = None
 
@@ -64,7 +71,7 @@ def lib() -> ctypes.CDLL:
         except ImportError:
             pass
         L = ctypes.CDLL(LIB_PATH)
-        vp, i64, ci = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
+        vp, i64, ci, cf = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float
         L.dg_gemm_fp8_blockscaled.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, ci, vp]
         L.dg_gemm_fp8_blockscaled.restype = ci
         L.dg_grouped_gemm_fp8.argtypes = [vp, vp, vp, vp, vp, vp, ci, i64, i64, i64, ci, vp]
@@ -93,6 +100,16 @@ def lib() -> ctypes.CDLL:
             "dg_swiglu_fp8": (ci, [vp, ci, vp, vp, vp, vp, i64, i64, vp]),
             "dg_swiglu_fp8_bwd": (ci, [vp, ci, vp, vp, vp, i64, i64, vp]),
             "dg_grouped_wgrad_fp8": (ci, [vp, vp, vp, vp, vp, ci, i64, i64, i64, vp, ci, ci, vp]),
+            "dg_moe_route": (ci, [vp, ci, vp, vp, i64, i64, ci, ci, ci, cf, vp, vp, vp, vp, vp, vp, vp, vp]),
+            "dg_moe_route_workspace": (i64, [i64, i64, ci]),
+            "dg_moe_route_bwd": (ci, [vp, vp, ci, vp, vp, vp, vp, i64, i64, ci, ci, ci, cf, vp, vp]),
+            "dg_residual_norm": (ci, [vp, ci, vp, ci, vp, vp, ci, cf, vp, cf, vp, vp, vp, vp, ci, i64, i64, vp]),
+            "dg_residual_norm_bwd": (ci, [vp, vp, vp, ci, vp, ci, vp, vp, ci, cf, vp, cf, vp, vp, vp, vp, vp, i64,
+                                          i64, vp, vp]),
+            "dg_residual_norm_bwd_workspace": (i64, [i64, i64, ci]),
+            "dg_grad_norm": (ci, [vp, vp, vp, ci, vp, vp, vp]),
+            "dg_grad_norm_workspace": (i64, [vp, vp, ci]),
+            "dg_clip_grads": (ci, [vp, vp, vp, ci, vp, cf, vp, vp, vp]),
         }
         for name, (result, arguments) in around.items():
             if hasattr(L, name):                  # a library of an earlier build may lack it; calling it then raises
@@ -190,6 +207,51 @@ def dg_grouped_wgrad_fp8(dY, X, sX, group_offsets, group_counts, num_groups, M_t
                          accumulate, stream) -> int:
     return lib().dg_grouped_wgrad_fp8(dY, X, sX, group_offsets, group_counts, num_groups, M_total, N, K, dW,
                                       out_dtype, accumulate, stream)
+
+
+def dg_moe_route(logits, dtype, bias, mask, T, E, top_k, score, renormalise, scale, ids, weights, counts, prob_sums,
+                 routed, loss, workspace, stream) -> int:
+    return lib().dg_moe_route(logits, dtype, bias, mask, T, E, top_k, score, renormalise, scale, ids, weights, counts,
+                              prob_sums, routed, loss, workspace, stream)
+
+
+def dg_moe_route_workspace(T, E, top_k) -> int:
+    return lib().dg_moe_route_workspace(T, E, top_k)
+
+
+def dg_moe_route_bwd(dweights, logits, dtype, ids, counts, routed, dloss, T, E, top_k, score, renormalise, scale,
+                     dlogits, stream) -> int:
+    return lib().dg_moe_route_bwd(dweights, logits, dtype, ids, counts, routed, dloss, T, E, top_k, score, renormalise,
+                                  scale, dlogits, stream)
+
+
+def dg_residual_norm(R, r_dtype, Y, dtype, w_post, gate, gate_kind, alpha, w_pre, eps, R_out, N, Q, S, scale_mode, T, H,
+                     stream) -> int:
+    return lib().dg_residual_norm(R, r_dtype, Y, dtype, w_post, gate, gate_kind, alpha, w_pre, eps, R_out, N, Q, S,
+                                  scale_mode, T, H, stream)
+
+
+def dg_residual_norm_bwd(dR, dN, R, r_dtype, Y, dtype, w_post, gate, gate_kind, alpha, w_pre, eps, dR_out, dY, dw_post,
+                         dgate, dw_pre, T, H, workspace, stream) -> int:
+    return lib().dg_residual_norm_bwd(dR, dN, R, r_dtype, Y, dtype, w_post, gate, gate_kind, alpha, w_pre, eps, dR_out,
+                                      dY, dw_post, dgate, dw_pre, T, H, workspace, stream)
+
+
+def dg_residual_norm_bwd_workspace(T, H, sums) -> int:
+    return lib().dg_residual_norm_bwd_workspace(T, H, sums)
+
+
+def dg_grad_norm(grads, sizes, dtypes, count, norm, workspace, stream) -> int:
+    """grads, sizes, dtypes: ctypes arrays of host memory."""
+    return lib().dg_grad_norm(grads, sizes, dtypes, count, norm, workspace, stream)
+
+
+def dg_grad_norm_workspace(sizes, dtypes, count) -> int:
+    return lib().dg_grad_norm_workspace(sizes, dtypes, count)
+
+
+def dg_clip_grads(grads, sizes, dtypes, count, norm, max_norm, outs, out_dtypes, stream) -> int:
+    return lib().dg_clip_grads(grads, sizes, dtypes, count, norm, max_norm, outs, out_dtypes, stream)
 
 
 def dg_status_string(status: int) -> str:
@@ -523,3 +585,104 @@ def grouped_wgrad_fp8(dY, X, sX, group_offsets, group_counts=None, out_dtype="f3
     dW; rows past group_counts are not used."""
     return _call("grouped_wgrad_fp8", stream, dY, X, sX, group_offsets, group_counts, out_code(out_dtype), dW,
                  accumulate)
+
+
+# ---------------------------------------------------------------- around a block of a model
+
+class MoERoute(NamedTuple):
+    """What moe_route finds out about one batch.  The last four are None without
+    `balance`; routed and loss have no dimensions."""
+    ids: object               # int32 [T][top_k], -1: no expert
+    weights: object           # float32 [T][top_k]
+    counts: object            # int32 [E] tokens that chose an expert
+    prob_sums: object         # float32 [E] the tokens' probabilities added up
+    routed: object            # int32 tokens with a choice
+    loss: object              # float32 balance loss
+
+
+class ResidualNorm(NamedTuple):
+    R: object                 # [T][H] the stream after the block, None without one
+    N: object                 # [T][H] its norm, None without `values` or w_pre
+    Q: object                 # uint8 [T][H] the norm's E4M3 codes, None without `codes`
+    S: object                 # float32 [T][ceil(H/128)] their scales
+
+
+class ResidualNormGrads(NamedTuple):
+    """None for what the forward call did not have."""
+    dR: object                # [T][H] of the stream before the block
+    dY: object                # [T][H]
+    dw_post: object           # float32 [H]
+    dgate: object             # float32, of gate's shape
+    dw_pre: object            # float32 [H]
+
+
+def score_code(score) -> int:
+    if score in (DG_SCORE_SOFTMAX, "softmax"):
+        return DG_SCORE_SOFTMAX
+    if score in (DG_SCORE_SIGMOID, "sigmoid"):
+        return DG_SCORE_SIGMOID
+    raise ValueError(f"unknown score {score!r}")
+
+
+def moe_route(logits, top_k, score="softmax", renormalise=True, scale=1.0, bias=None, mask=None, balance=True,
+              stream=None):
+    """The MoERoute of router logits[T][E] (float32 or bfloat16; -inf closes an expert
+    to a token): each token's top_k experts, largest first, and their weights,
+    scale s_j, with `renormalise` divided by the chosen scores' sum.  score:
+    "softmax" or "sigmoid".  bias float32 [E] is added to the scores for the choice
+    alone.  mask bool [T]: False for rows that hold no token.  balance: also the
+    experts' load and the balance loss E / (top_k n^2) sum counts_e prob_sums_e."""
+    return MoERoute(*_call("moe_route", stream, logits, top_k, score_code(score), renormalise, scale, bias, mask,
+                           balance))
+
+
+def moe_route_bwd(dweights, logits, ids, score="softmax", renormalise=True, scale=1.0, dloss=None, counts=None,
+                  routed=None, dlogits=None, stream=None):
+    """The gradient of the logits from dweights[T][top_k] (float32) and dloss (a
+    float32 tensor of one element, with moe_route's counts and routed, or their sums
+    over several devices)."""
+    return _call("moe_route_bwd", stream, dweights, logits, ids, score_code(score), renormalise, scale, dloss, counts,
+                 routed, dlogits)
+
+
+def _dtype_code(dtype):
+    torch = _torch()
+    if dtype in (None, "bf16", "bfloat16", torch.bfloat16):
+        return DG_IN_BF16
+    if dtype in ("f32", "float32", torch.float32):
+        return DG_IN_F32
+    raise ValueError(f"unknown dtype {dtype!r}")
+
+
+def residual_norm(R, Y=None, w_post=None, gate=None, alpha=1.0, w_pre=None, eps=1e-6, values=True, codes=None,
+                  dtype=None, stream=None):
+    """The residual stream R[T][H] past a block with output Y[T][H], and the norm before
+    the next one: R' = R + alpha gate rms(Y, w_post), N = rms(R', w_pre), with
+    rms(v, w) = w v / sqrt(mean(v^2) + eps).  Weights are float32 [H]; gate float32,
+    [H] by channel or [T][1] by token.  R and Y are float32 or bfloat16, each its own.
+    Y None: no block before (R' is R).  w_post None: Y as it is.  w_pre None: no norm.
+    values: N as values of `dtype` (Y's; without Y bfloat16 if None); codes: "pow2" or
+    "amax": also as E4M3 codes with a scale per row and 128 columns, A and sA of the
+    products."""
+    mode = -1 if codes is None else scale_code(codes)
+    code = -1 if Y is not None and dtype is None else _dtype_code(dtype)
+    return ResidualNorm(*_call("residual_norm", stream, R, Y, w_post, gate, alpha, w_pre, eps, values, mode, code))
+
+
+def residual_norm_bwd(dR, dN, R, Y=None, w_post=None, gate=None, alpha=1.0, w_pre=None, eps=1e-6, stream=None):
+    """The ResidualNormGrads of residual_norm from the gradients dR of R' (None: zeros)
+    and dN of N (None without w_pre).  R is the stream that the forward call returned,
+    R' (its input where there was no block); without w_pre it may be None."""
+    return ResidualNormGrads(*_call("residual_norm_bwd", stream, dR, dN, R, Y, w_post, gate, alpha, w_pre, eps))
+
+
+def grad_norm(grads, stream=None):
+    """sqrt of the sum of all elements' squares over a list of tensors (float32 or
+    bfloat16), a float32 tensor without dimensions; nothing waits for the device."""
+    return _call("grad_norm", stream, grads)
+
+
+def clip_grads(grads, norm, max_norm, out=None, stream=None):
+    """The gradients times min(1, max_norm / norm), norm as grad_norm returns it: in
+    place, or into the tensors `out`, of the same shapes (float32 or bfloat16)."""
+    return _call("clip_grads", stream, grads, norm, max_norm, out)
