@@ -35,7 +35,7 @@ namespace dg {
   DG_BLOCK_KERNEL(dg_moe_route_bwd_##T##_64x16, kRouteBwdThreads, RouteBwdArgs, route_bwd_body<BF16, 64, 16>)
 DG_ROUTE_KERNELS(bf16, true)
 DG_ROUTE_KERNELS(f32, false)
-DG_BLOCK_KERNEL(dg_moe_route_finish, kRouteThreads, RouteArgs, route_finish)
+DG_BLOCK_KERNEL(dg_moe_route_finish, kFinishExperts * kFinishParts, RouteArgs, route_finish_body)
 #undef DG_ROUTE_KERNELS
 
 // (templates: stream and value types, codes, whole rows, wide rows)
@@ -218,7 +218,7 @@ extern "C" {
 int64_t dg_moe_route_workspace(int64_t T, int64_t E, int top_k) {
   const int st = check_route(T, E, top_k);
   if (st != DG_OK) return st;
-  return route_blocks(T, E, top_k, true) * (8 * E + 4);
+  return route_blocks(T, E, top_k, true) * (8 * E + 4) + 8 * E + 4;
 }
 
 int dg_moe_route(const void* logits, int dtype, const float* bias, const uint8_t* mask, int64_t T, int64_t E, int top_k,
@@ -232,14 +232,16 @@ int dg_moe_route(const void* logits, int dtype, const float* bias, const uint8_t
     return DG_ERR_INVALID_ARG;
   if (!aligned(counts, 4) || !aligned(prob_sums, 4) || !aligned(routed, 4) || !aligned(loss, 4) || !aligned(bias, 4))
     return DG_ERR_INVALID_ARG;
-  if (balance && bad(workspace, 4)) return DG_ERR_INVALID_ARG;
+  if (balance && bad(workspace, 8)) return DG_ERR_INVALID_ARG;
   if (T > 0 && (bad(logits, 16) || bad(ids, 4) || bad(weights, 4))) return DG_ERR_INVALID_ARG;
   if (T == 0 && !balance) return DG_OK;
   const int64_t nb = route_blocks(T, E, top_k, balance);
-  float* part = static_cast<float*>(workspace);
-  int32_t* ints = reinterpret_cast<int32_t*>(part) + nb * E;
-  dg::RouteArgs a{logits, bias, mask, ids, weights, counts, prob_sums, routed, loss, part, ints, ints + nb * E,
-                  int(T), int(E), top_k, int(nb), score == DG_SCORE_SIGMOID, renormalise, scale};
+  double* terms = static_cast<double*>(workspace);
+  float* part = reinterpret_cast<float*>(terms + E);
+  int32_t* ints = reinterpret_cast<int32_t*>(part + nb * E);
+  dg::RouteArgs a{logits, bias, mask, ids, weights, counts, prob_sums, routed, loss, part, ints, ints + nb * E, terms,
+                  ints + nb * E + nb, int(T), int(E), top_k, int(nb), score == DG_SCORE_SIGMOID, renormalise,
+                  aligned(bias, 16), scale};
 #define DG_ROUTE_TABLE(T)                                                                                       \
   {{dg::dg_moe_route_##T##_16x4, dg::dg_moe_route_##T##_16x16, dg::dg_moe_route_##T##_64x4,                     \
     dg::dg_moe_route_##T##_64x16},                                                                              \
@@ -250,7 +252,7 @@ int dg_moe_route(const void* logits, int dtype, const float* bias, const uint8_t
   const int st1 = launch(kernels[dtype == DG_IN_BF16][bias != nullptr][route_variant(E, top_k)], a, nb,
                          dg::kRouteThreads, stream);
   if (st1 != DG_OK || !balance) return st1;
-  return launch(dg::dg_moe_route_finish, a, 1, dg::kRouteThreads, stream);
+  return launch(dg::dg_moe_route_finish, a, ceil_div(E, dg::kFinishExperts), dg::kFinishExperts * dg::kFinishParts, stream);
 }
 
 int dg_moe_route_bwd(const float* dweights, const void* logits, int dtype, const int32_t* ids, const int32_t* counts,

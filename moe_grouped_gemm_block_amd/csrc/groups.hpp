@@ -60,6 +60,14 @@ __device__ __forceinline__ T group_reduce(T v, F f) {
   return v;
 }
 
+// v of lane I of the row of 16
+template <int I, typename T>
+__device__ __forceinline__ T row_broadcast(T v) {
+  static_assert(sizeof(T) == 4, "one register");
+  const int b = __builtin_bit_cast(int, v);
+  return __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(b, b, 0x150 + I, 0xF, 0xF, false));
+}
+
 template <int L, typename T>
 __device__ __forceinline__ T group_sum(T v) {
   return group_reduce<L>(v, [](T a, T b) { return a + b; });

@@ -18,8 +18,9 @@
 // them (softmax) or that and 0, whichever is less (sigmoid), so that no share is
 // 0 / 0 where all scores underflow.
 //
-// A group of L lanes takes a token, V logits per lane, lane l those from l V on: the
-// lowest lane that holds the largest value then also holds the lowest index.
+// A group of L lanes takes a token, V logits per lane in pieces of four, which lie side by
+// side over the lanes: lane l's v-th is logit 4 L (v / 4) + 4 l + v % 4, so that loads and
+// stores are of whole lines.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -51,8 +52,10 @@ struct RouteArgs {
   float* part_sums;          // [nb][E]
   int32_t* part_counts;      // [nb][E]
   int32_t* part_routed;      // [nb]
+  double* terms;             // [E] counts_e P_e
+  int32_t* done;             // workgroups of the last step that have ended
   int T, E, k, nb;
-  int sigmoid, renorm;
+  int sigmoid, renorm, bias_aligned;
   float scale;
 };
 
@@ -96,40 +99,45 @@ __device__ __forceinline__ float key_value(uint32_t key) {
   return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
 }
 
-// V logits from element e0 of a row on, -inf past its end.  `whole`: rows of a
-// multiple of V logits, which then lie in or out together.
-template <bool BF16, int V>
-__device__ __forceinline__ void load_logits(const void* x, size_t row, int e0, int E, bool whole, float (&v)[V]) {
-  if (whole && e0 < E) {
-    if constexpr (BF16) {
-      const uint16_t* src = static_cast<const uint16_t*>(x) + row + e0;
+template <bool BF16>
+__device__ __forceinline__ float logit(const void* x, size_t i) {
+  if constexpr (BF16) return __uint_as_float(uint32_t(static_cast<const uint16_t*>(x)[i]) << 16);
+  else return static_cast<const float*>(x)[i];
+}
+
+// Logit of lane l's v-th value, and back.
+template <int L>
+__device__ __forceinline__ int expert_of(int l, int v) { return 4 * L * (v / 4) + 4 * l + v % 4; }
+template <int L>
+__device__ __forceinline__ int lane_of(int e) { return e / 4 % L; }
+template <int L>
+__device__ __forceinline__ int value_of(int e) { return e / (4 * L) * 4 + e % 4; }
+
+// A lane's V values of a row of E, `none` past its end.  `whole`: rows of a multiple of
+// four values, aligned to four.
+template <bool BF16, int L, int V>
+__device__ __forceinline__ void load_row(const void* x, size_t row, int l, int E, bool whole, float none, float (&v)[V]) {
 #pragma unroll
-      for (int i = 0; i < V / 4; ++i) {
-        const uint2 w = reinterpret_cast<const uint2*>(src)[i];
-        v[4 * i] = __uint_as_float(w.x << 16);
-        v[4 * i + 1] = __uint_as_float(w.x & 0xFFFF0000u);
-        v[4 * i + 2] = __uint_as_float(w.y << 16);
-        v[4 * i + 3] = __uint_as_float(w.y & 0xFFFF0000u);
+  for (int i = 0; i < V / 4; ++i) {
+    const int e = expert_of<L>(l, 4 * i);
+    float* o = v + 4 * i;
+    if (whole && e < E) {
+      if constexpr (BF16) {
+        const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(x) + row + e);
+        o[0] = __uint_as_float(w.x << 16);
+        o[1] = __uint_as_float(w.x & 0xFFFF0000u);
+        o[2] = __uint_as_float(w.y << 16);
+        o[3] = __uint_as_float(w.y & 0xFFFF0000u);
+      } else {
+        const float4 w = *reinterpret_cast<const float4*>(static_cast<const float*>(x) + row + e);
+        o[0] = w.x;
+        o[1] = w.y;
+        o[2] = w.z;
+        o[3] = w.w;
       }
     } else {
-      const float* src = static_cast<const float*>(x) + row + e0;
 #pragma unroll
-      for (int i = 0; i < V / 4; ++i) {
-        const float4 w = reinterpret_cast<const float4*>(src)[i];
-        v[4 * i] = w.x;
-        v[4 * i + 1] = w.y;
-        v[4 * i + 2] = w.z;
-        v[4 * i + 3] = w.w;
-      }
-    }
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    v[i] = -__builtin_inff();
-    if (e0 + i < E) {
-      if constexpr (BF16) v[i] = __uint_as_float(uint32_t(static_cast<const uint16_t*>(x)[row + e0 + i]) << 16);
-      else v[i] = static_cast<const float*>(x)[row + e0 + i];
+      for (int c = 0; c < 4; ++c) o[c] = e + c < E ? logit<BF16>(x, row + e + c) : none;
     }
   }
 }
@@ -163,66 +171,40 @@ __device__ __forceinline__ T pick(const T (&a)[V], int i) {
   return pick_of(a, i, std::make_integer_sequence<int, V>{});
 }
 
-// Choices by score + bias.  The sums are compared in FP32 first: a score is off by at
-// most 2^-21 of itself (sigmoid), or 2^-18 (softmax: the terms' 2^-22 and up to 22
-// roundings of their sum's 2^-24, and of e^(x - m) what x - m rounded to costs), and
-// none is larger than `most`; the sum with the bias rounds once.  Where two sums that
-// follow each other are closer than twice that, the choice is made again with those that
-// are that close to the largest compared in 64 bits.
+// ---- choice -----------------------------------------------------------------------
+// A value's order key with its lowest bits replaced by the expert's number, the lower
+// number larger: the largest of a group names its expert, and taking it out is one
+// comparison per register, where a search for the index beside whole keys takes another
+// 36 instructions a choice.  What the lost bits leave open is settled afterwards: the
+// choices go on past the k-th until one is certainly smaller than the one before, and
+// where two in a row were too close to tell, lane j computes the j-th one's whole key, and
+// they are ranked by those.  BF16 logits lose nothing.  Where more than a lane each are
+// too close (rows of equal logits) the choice is made again with whole keys throughout.
+//
+// With a bias a key is of an FP32 approximation of s + bias, and the whole key of s +
+// bias in 64 bits.  A score is off by at most 2^-21 of itself (sigmoid) or 2^-18
+// (softmax: the terms' 2^-22 and up to 22 roundings of their sum's 2^-24, and what x - m
+// rounded to costs), none is larger than `most`, and the sum with the bias rounds once.
 __device__ __forceinline__ float biased_tolerance(float largest, float most, bool sigmoid) {
   return (sigmoid ? 0x1p-19f : 0x1p-16f) * most + 0x1p-22f * __builtin_fabsf(largest);
-}
-
-// One workgroup of kRouteThreads: the partial sums of all workgroups added up in
-// their order, and the loss in 64 bits.
-__device__ __forceinline__ void route_finish(const RouteArgs& p) {
-  __shared__ double terms[kRouteWaves];
-  __shared__ int ns[kRouteWaves];
-  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-  double term = 0.0;
-  for (int e = t; e < p.E; e += kRouteThreads) {
-    float sum = 0.f;
-    int count = 0;
-    for (int b = 0; b < p.nb; ++b) {
-      sum += p.part_sums[size_t(b) * p.E + e];
-      count += p.part_counts[size_t(b) * p.E + e];
-    }
-    p.sums[e] = sum;
-    p.counts[e] = count;
-    term += double(sum) * count;
-  }
-  int n = 0;
-  for (int b = t; b < p.nb; b += kRouteThreads) n += p.part_routed[b];
-  term = group_sum<64>(term);
-  n = group_sum<64>(n);
-  if (lane == 0) {
-    terms[wave] = term;
-    ns[wave] = n;
-  }
-  __syncthreads();
-  if (t == 0) {
-    for (int w = 1; w < kRouteWaves; ++w) {
-      term += terms[w];
-      n += ns[w];
-    }
-    *p.routed = n;
-    *p.loss = n ? float(term * p.E / (double(p.k) * n * n)) : 0.f;
-  }
 }
 
 template <bool BF16, int L, int V, bool BIASED>
 __device__ __forceinline__ void route_body(const RouteArgs& p) {
   constexpr int PER_WAVE = 64 / L, PER_BLOCK = kRouteWaves * PER_WAVE;
+  constexpr uint32_t NUMBER = L * V - 1;            // bits of an expert's number
+  constexpr bool WHOLE_KEYS = BF16 && !BIASED;      // all of a key is above them
   __shared__ int32_t count[L * V];
-  __shared__ float part[kRouteWaves][L * V];             // expert l V + v at v L + l: no bank conflicts
+  __shared__ float part[kRouteWaves][L * V];        // lane l's v-th at v L + l: no bank conflicts
   __shared__ int routed_of[kRouteWaves];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int l = lane & (L - 1), base = lane & ~(L - 1);
-  const int e0 = l * V;
-  const bool balance = p.counts != nullptr, sigmoid = p.sigmoid != 0, whole = p.E % V == 0;
+  const bool balance = p.counts != nullptr, sigmoid = p.sigmoid != 0, whole = p.E % 4 == 0;
+  const float inf = __builtin_inff();
   if (balance) {
     for (int e = threadIdx.x; e < L * V; e += kRouteThreads) count[e] = 0;
     for (int i = lane; i < L * V; i += 64) part[wave][i] = 0.f;     // (the wave's own)
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.done = 0;
     __syncthreads();
   }
   int routed_sum = 0;
@@ -231,12 +213,13 @@ __device__ __forceinline__ void route_body(const RouteArgs& p) {
   for (long long t0 = (long long)blockIdx.x * PER_BLOCK; t0 < p.T; t0 += (long long)p.nb * PER_BLOCK) {
     const long long t = t0 + wave * PER_WAVE + lane / L;
     const bool there = t < p.T && (p.mask == nullptr || p.mask[t] != 0);
+    const size_t row = size_t(t) * p.E;
     float x[V];
     if (there) {
-      load_logits<BF16, V>(p.x, size_t(t) * p.E, e0, p.E, whole, x);
+      load_row<BF16, L, V>(p.x, row, l, p.E, whole, -inf, x);
     } else {
 #pragma unroll
-      for (int v = 0; v < V; ++v) x[v] = -__builtin_inff();
+      for (int v = 0; v < V; ++v) x[v] = -inf;
     }
     uint32_t key[V];
     uint32_t top = 0;
@@ -246,18 +229,18 @@ __device__ __forceinline__ void route_body(const RouteArgs& p) {
       top = max(top, key[v]);
     }
     top = group_max<L>(top);
-    const bool open = top != 0;
-    const float m = open ? key_value(top) : 0.f;
+    const float m = top ? key_value(top) : 0.f;
 
     // scores of all experts (over e^min(m, 0) or e^m), where something needs them; they
     // are not kept in registers during the choice
-    bool routed = open;
+    bool routed = top != 0;
     float z = 1.f;
-    [[maybe_unused]] float f = 1.f;                // what makes them scores
+    [[maybe_unused]] float f = 1.f;                 // what makes them scores
     [[maybe_unused]] auto biased_keys = [&](const float (&s)[V]) {
+      float bias[V];
+      load_row<false, L, V>(p.bias, 0, l, p.E, whole && p.bias_aligned, 0.f, bias);
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-        key[v] = x[v] == -__builtin_inff() ? 0u : order_key(__builtin_fmaf(s[v], f, p.bias[min(e0 + v, p.E - 1)]));
+      for (int v = 0; v < V; ++v) key[v] = x[v] == -inf ? 0u : order_key(__builtin_fmaf(s[v], f, bias[v]));
     };
     if (BIASED || balance || (!p.renorm && !sigmoid)) {
       float s[V];
@@ -268,15 +251,15 @@ __device__ __forceinline__ void route_body(const RouteArgs& p) {
         z += s[v];
       }
       z = group_sum<L>(z);
-      if (!open) z = 1.f;
+      if (top == 0) z = 1.f;
       const float r = 1.f / z;
       if constexpr (BIASED) {
         f = sigmoid ? exp_nonpos(fminf(m, 0.f)) : r;
         biased_keys(s);
-        bool some = false;                         // a bias of -inf may have closed the open ones
+        uint32_t some = 0;                          // a bias of -inf may have closed the open ones
 #pragma unroll
-        for (int v = 0; v < V; ++v) some = some || key[v] != 0;
-        routed = ((__ballot(some) >> base) & (L == 64 ? ~uint64_t(0) : uint64_t(0xFFFF))) != 0;
+        for (int v = 0; v < V; ++v) some |= key[v];
+        routed = group_max<L>(some) != 0;
       }
       if (balance) {
 #pragma unroll
@@ -292,102 +275,137 @@ __device__ __forceinline__ void route_body(const RouteArgs& p) {
     }
 
     // lane j of the group takes choice j
-    int id = -1;
-    float xs = -__builtin_inff();
-    auto take = [&](int j, uint32_t g, uint64_t who, int sel) {
-      const int w = __builtin_ctzll(who >> base);       // the lowest lane of the group
-      float xsel = 0.f;
-      if constexpr (BIASED) xsel = __shfl(pick(x, sel), base + w, 64);
-      else xsel = key_value(g);
+    const float most = sigmoid ? 1.f : f;
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (l == w && v == sel) key[v] = 0;
-      sel = __shfl(sel, base + w, 64);
-      if (l == j && g != 0) {
-        id = w * V + sel;
-        xs = xsel;
-      }
-    };
-    // the largest key of the group, and where this lane has it first
-    auto largest = [&](int& sel, uint64_t& who) {
+    for (int v = 0; v < V; ++v)
+      key[v] = key[v] ? (key[v] & ~NUMBER) | (NUMBER - uint32_t(expert_of<L>(l, v))) : 0u;
+    uint32_t mine = 0;
+    [[maybe_unused]] uint32_t before = 0;
+    [[maybe_unused]] bool close = false, more = false;
+    int n = p.k;                                    // choices that there are
+    for (int j = 0; WHOLE_KEYS ? j < p.k : j <= L; ++j) {
       uint32_t best = 0;
 #pragma unroll
       for (int v = 0; v < V; ++v) best = max(best, key[v]);
       const uint32_t g = group_max<L>(best);
-      who = __ballot(best == g);
-      sel = 0;
-#pragma unroll
-      for (int v = V - 1; v >= 0; --v) sel = key[v] == g ? v : sel;
-      return g;
-    };
-    if constexpr (!BIASED) {
-      for (int j = 0; j < p.k; ++j) {
-        int sel;
-        uint64_t who;
-        const uint32_t g = largest(sel, who);
-        take(j, g, who, sel);
-      }
-    } else {
-      const float most = sigmoid ? 1.f : f;
-      bool close = false;
-      float before = 0.f;
-      for (int j = 0; j <= p.k; ++j) {
-        int sel;
-        uint64_t who;
-        const uint32_t g = largest(sel, who);
-        const float now = key_value(g);
-        if (j > 0 && g != 0) close = close || !(before - now > biased_tolerance(before, most, sigmoid));
-        before = now;
-        if (j < p.k) take(j, g, who, sel);
-      }
-      if (__ballot(close)) {
-        float s[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) s[v] = shifted_score(x[v], m, sigmoid);
-        biased_keys(s);
-        id = -1;
-        double z64 = 1.0;
-        if (!sigmoid) {
-          z64 = 0.0;
-#pragma unroll 1
-          for (int v = 0; v < V; ++v) z64 += exp_nonpos(double(pick(x, v)) - double(m));
-          z64 = group_sum<L>(z64);
+      if constexpr (!WHOLE_KEYS) {
+        more = false;
+        if (j > 0 && g != 0) {
+          const uint32_t high = g | NUMBER, low = before & ~NUMBER;   // bounds of their keys
+          if constexpr (BIASED) more = !(key_value(low) - key_value(high) > biased_tolerance(key_value(low), most, sigmoid));
+          else more = high >= low;
         }
+        if (j >= p.k && !__ballot(more)) {
+          n = j;
+          break;
+        }
+        close = close || more;
+        n = j;
+        before = g;
+      }
+      if (l == j) mine = g;
+#pragma unroll
+      for (int v = 0; v < V; ++v) key[v] = key[v] == g ? 0u : key[v];
+    }
+    int id = mine ? int(NUMBER - (mine & NUMBER)) : -1;
+
+    if constexpr (!WHOLE_KEYS) {
+      // s + bias in 64 bits
+      double z64 = 1.0;
+      [[maybe_unused]] auto all64 = [&] {
+        if (sigmoid) return;
+        z64 = 0.0;
+#pragma unroll 1
+        for (int v = 0; v < V; ++v) z64 += exp_nonpos(double(pick(x, v)) - double(m));
+        z64 = group_sum<L>(z64);
+      };
+      [[maybe_unused]] auto sum64 = [&](float xv, float bias) {
+        const double e = exp_nonpos(sigmoid ? -__builtin_fabs(double(xv)) : double(xv) - double(m));
+        return (sigmoid && xv > 0.f ? 1.0 : e) / (sigmoid ? 1.0 + e : z64) + double(bias);
+      };
+      if (__ballot(close) && !__ballot(more)) {
+        // the n choices ranked by their whole keys, equal ones by their numbers; lanes
+        // without a choice behind them
+        uint64_t kd = 0;
+        if constexpr (BIASED) all64();
+        if (l < n && id >= 0) {
+          const float xv = logit<BF16>(p.x, row + id);
+          if constexpr (BIASED) kd = order_key(sum64(xv, p.bias[id]));
+          else kd = order_key(xv);
+        }
+        const int number = l < n && id >= 0 ? id : int(NUMBER) + 1 + l;
+        int rank = 0;
+        for (int i = 0; i < n; ++i) {
+          const uint64_t ki = __shfl(kd, base + i, 64);
+          const int ni = __shfl(number, base + i, 64);
+          rank += ki > kd || (ki == kd && ni < number);
+        }
+        if (l >= n) rank = l;
+        id = __builtin_amdgcn_ds_permute((base + rank) << 2, id);
+      } else if (__ballot(close)) {
+        // whole keys throughout
+        if constexpr (BIASED) {
+          float s[V];
+#pragma unroll
+          for (int v = 0; v < V; ++v) s[v] = shifted_score(x[v], m, sigmoid);
+          biased_keys(s);
+          all64();
+        } else {
+#pragma unroll
+          for (int v = 0; v < V; ++v) key[v] = order_key(x[v]);
+        }
+        id = -1;
 #pragma unroll 1
         for (int j = 0; j < p.k; ++j) {
-          int sel;
-          uint64_t who;
-          const uint32_t g = largest(sel, who);
-          const float now = key_value(g), cut = now - biased_tolerance(now, most, sigmoid);
-          uint32_t near = 0;
+          uint32_t best = 0;
 #pragma unroll
-          for (int v = 0; v < V; ++v) near |= uint32_t(key[v] != 0 && !(key_value(key[v]) < cut)) << v;
-          if (__ballot(group_sum<L>(__popc(near)) > 1)) {
-            uint64_t best = 0;
+          for (int v = 0; v < V; ++v) best = max(best, key[v]);
+          const uint32_t g = group_max<L>(best);
+          // the lane's first of the largest
+          int e = INT32_MAX;
+          if constexpr (BIASED) {
+            const float cut = key_value(g) - biased_tolerance(key_value(g), most, sigmoid);
+            uint32_t near = 0;
+#pragma unroll
+            for (int v = 0; v < V; ++v) near |= uint32_t(key[v] != 0 && !(key_value(key[v]) < cut)) << v;
+            uint64_t kd = 0;
+            float x_of = 0.f, bias_of = 0.f;        // what kd is of: the same again changes nothing
             while (__ballot(near != 0)) {
               const int v = near ? __builtin_ctz(near) : 0;
-              const double xv = pick(x, v);
-              const double e = exp_nonpos(sigmoid ? -__builtin_fabs(xv) : xv - double(m));
-              const double sv = (sigmoid && xv > 0.0 ? 1.0 : e) / (sigmoid ? 1.0 + e : z64);
-              const uint64_t kd = order_key(sv + double(p.bias[min(e0 + v, p.E - 1)]));
-              if (near != 0 && kd > best) {
-                best = kd;
-                sel = v;
+              const int ev = expert_of<L>(l, v);
+              const float xv = pick(x, v), bv = p.bias[near ? ev : 0];
+              const bool other = near != 0 && !(kd != 0 && xv == x_of && bv == bias_of);
+              if (__ballot(other)) {
+                const uint64_t kv = order_key(sum64(xv, bv));
+                if (other && kv > kd) {
+                  kd = kv;
+                  e = ev;
+                  x_of = xv;
+                  bias_of = bv;
+                }
               }
               near &= near - 1;
             }
-            who = __ballot(best == group_max<L>(best));
+            if (kd != group_max<L>(kd)) e = INT32_MAX;
+          } else {
+#pragma unroll
+            for (int v = V - 1; v >= 0; --v) e = key[v] == g ? expert_of<L>(l, v) : e;
           }
-          take(j, g, who, sel);
+          e = group_reduce<L>(e, [](int a, int b) { return a < b ? a : b; });
+          if (l == j && g != 0) id = e;
+#pragma unroll
+          for (int v = 0; v < V; ++v) key[v] = expert_of<L>(l, v) == e ? 0u : key[v];
         }
       }
     }
-
+    if (l >= p.k) id = -1;
     routed_sum += routed && l == 0;
 
+    // weights, from the choices' logits (in the caches still)
+    const float xs = id >= 0 ? logit<BF16>(p.x, row + id) : -inf;
     float w = 0.f;
     if (p.renorm) {
-      uint32_t tc = l < p.k ? order_key(xs) : 0;
+      uint32_t tc = order_key(xs);
       tc = group_max<L>(tc);
       const float mc = tc ? key_value(tc) : 0.f;
       const float s = id >= 0 ? shifted_score(xs, mc, sigmoid) : 0.f;
@@ -411,7 +429,7 @@ __device__ __forceinline__ void route_body(const RouteArgs& p) {
   for (int e = threadIdx.x; e < p.E; e += kRouteThreads) {
     float sum = 0.f;
 #pragma unroll
-    for (int w = 0; w < kRouteWaves; ++w) sum += part[w][e % V * L + e / V];
+    for (int w = 0; w < kRouteWaves; ++w) sum += part[w][value_of<L>(e) * L + lane_of<L>(e)];
     p.part_sums[size_t(blockIdx.x) * p.E + e] = sum;
     p.part_counts[size_t(blockIdx.x) * p.E + e] = count[e];
   }
@@ -419,6 +437,57 @@ __device__ __forceinline__ void route_body(const RouteArgs& p) {
     int n = 0;
     for (int w = 0; w < kRouteWaves; ++w) n += routed_of[w];
     p.part_routed[blockIdx.x] = n;
+  }
+}
+
+// The partial sums of all workgroups added up in their order, 32 experts a workgroup and
+// 32 threads an expert, and by the workgroup that ends last the loss, in 64 bits.
+// (Which one that is does not show: it adds the experts' terms in their order.)
+constexpr int kFinishExperts = 32;
+constexpr int kFinishParts = 32;
+
+__device__ __forceinline__ void route_finish_body(const RouteArgs& p) {
+  __shared__ float sums[kFinishParts][kFinishExperts + 1];
+  __shared__ int32_t counts[kFinishParts][kFinishExperts + 1];
+  __shared__ bool last;
+  const int col = threadIdx.x % kFinishExperts, part = threadIdx.x / kFinishExperts;
+  const int e = blockIdx.x * kFinishExperts + col;
+  float sum = 0.f;
+  int count = 0;
+  if (e < p.E) {
+#pragma unroll 8
+    for (int b = part; b < p.nb; b += kFinishParts) {
+      sum += p.part_sums[size_t(b) * p.E + e];
+      count += p.part_counts[size_t(b) * p.E + e];
+    }
+  }
+  sums[part][col] = sum;
+  counts[part][col] = count;
+  __syncthreads();
+  if (part == 0 && e < p.E) {
+    for (int i = 1; i < kFinishParts; ++i) {
+      sum += sums[i][col];
+      count += counts[i][col];
+    }
+    p.sums[e] = sum;
+    p.counts[e] = count;
+    p.terms[e] = double(sum) * count;
+    __threadfence();
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) last = atomicAdd(p.done, 1) == int(gridDim.x) - 1;
+  __syncthreads();
+  if (!last || threadIdx.x >= 64) return;
+  __threadfence();
+  double term = 0.0;
+  for (int i = threadIdx.x; i < p.E; i += 64) term += __hip_atomic_load(&p.terms[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  int n = 0;
+  for (int b = threadIdx.x; b < p.nb; b += 64) n += p.part_routed[b];
+  term = group_sum<64>(term);
+  n = group_sum<64>(n);
+  if (threadIdx.x == 0) {
+    *p.routed = n;
+    *p.loss = n ? float(term * p.E / (double(p.k) * n * n)) : 0.f;
   }
 }
 
@@ -445,39 +514,39 @@ constexpr int kRouteBwdThreads = 256;
 //   sigmoid, plain   u_j = scale s_j (1 - s_j) dw_j
 //   loss             f_e = dloss E / (k n^2) counts_e: p_e (f_e - sum p f) [(1 - s_e)]
 // A token without choices, and rows of the logits that it alone would read, add
-// nothing.  An expert that a token names twice gets both gradients.
+// nothing.  An expert that a token names twice gets both gradients, in their order.
+// The u_j reach their experts' lanes through LDS.
 template <bool BF16, int L, int V>
 __device__ __forceinline__ void route_bwd_body(const RouteBwdArgs& p) {
   constexpr int PER_BLOCK = kRouteBwdThreads / L;
+  __shared__ __attribute__((aligned(16))) float at_expert[PER_BLOCK][L * V];
   const int lane = threadIdx.x & 63;
   const int l = lane & (L - 1), base = lane & ~(L - 1);
-  const int e0 = l * V;
-  const bool sigmoid = p.sigmoid != 0, whole = p.E % V == 0, loss = p.counts != nullptr;
+  const bool sigmoid = p.sigmoid != 0, whole = p.E % 4 == 0, loss = p.counts != nullptr;
   const long long t = (long long)block_index() * PER_BLOCK + threadIdx.x / L;
   const bool in = t < p.T;
+  const size_t row = size_t(t) * p.E;
+  const float inf = __builtin_inff();
   int id = in && l < p.k ? p.ids[t * p.k + l] : -1;
   if (id >= p.E) id = -1;
   const uint64_t any = __ballot(id >= 0) >> base;
   const bool routed = (L == 64 ? any : any & 0xFFFFu) != 0;
-  float xs = -__builtin_inff(), dw = 0.f;
+  float xs = -inf, dw = 0.f;
   if (id >= 0) {
-    if constexpr (BF16) xs = __uint_as_float(uint32_t(static_cast<const uint16_t*>(p.x)[size_t(t) * p.E + id]) << 16);
-    else xs = static_cast<const float*>(p.x)[size_t(t) * p.E + id];
+    xs = logit<BF16>(p.x, row + id);
     dw = p.scale * p.dw[t * p.k + l];
   }
 
-  // what every expert gets: p_e (f_e - off)
-  float pe[V], f[V], off = 0.f, z = 1.f, m = 0.f;
-#pragma unroll
-  for (int v = 0; v < V; ++v) pe[v] = f[v] = 0.f;
-  float x[V];
+  // what every expert gets: p_e (f_e - off), for sigmoid times 1 - s_e
+  float pe[V], f[V], rest[V], off = 0.f, z = 1.f, m = 0.f;
   const bool all = loss || !(p.renorm || sigmoid);
   if (all) {
+    float x[V];
     if (routed) {
-      load_logits<BF16, V>(p.x, size_t(t) * p.E, e0, p.E, whole, x);
+      load_row<BF16, L, V>(p.x, row, l, p.E, whole, -inf, x);
     } else {
 #pragma unroll
-      for (int v = 0; v < V; ++v) x[v] = -__builtin_inff();
+      for (int v = 0; v < V; ++v) x[v] = -inf;
     }
     uint32_t top = 0;
 #pragma unroll
@@ -488,19 +557,23 @@ __device__ __forceinline__ void route_bwd_body(const RouteBwdArgs& p) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       pe[v] = shifted_score(x[v], m, sigmoid);
+      rest[v] = sigmoid ? one_minus_sigmoid(x[v]) : 1.f;
       z += pe[v];
     }
     z = group_sum<L>(z);
     if (top == 0) z = 1.f;                  // no expert of the row is open
     const float r = 1.f / z;
 #pragma unroll
-    for (int v = 0; v < V; ++v) pe[v] *= r;
+    for (int v = 0; v < V; ++v) {
+      pe[v] *= r;
+      f[v] = 0.f;
+    }
     if (loss) {
       const double n = *p.routed;
       const float c = n > 0.0 ? float(double(*p.dloss) * p.E / (double(p.k) * n * n)) : 0.f;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        f[v] = c * float(p.counts[e0 + v < p.E ? e0 + v : 0]);
+        f[v] = c * float(p.counts[min(expert_of<L>(l, v), p.E - 1)]);
         off = __builtin_fmaf(pe[v], f[v], off);
       }
       off = group_sum<L>(off);
@@ -526,31 +599,51 @@ __device__ __forceinline__ void route_bwd_body(const RouteBwdArgs& p) {
     }
   }
   if (!p.renorm && !sigmoid) off += group_sum<L>(u);
-  if (id < 0) u = 0.f;
 
-  float d[V];
+  // (a wave reads and writes its own tokens' rows only)
+  float* mine = at_expert[threadIdx.x / L];
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    d[v] = 0.f;
-    if (all) {
-      d[v] = pe[v] * (f[v] - off);
-      if (sigmoid) d[v] *= one_minus_sigmoid(x[v]);
+  for (int i = 0; i < V / 4; ++i) *reinterpret_cast<float4*>(mine + expert_of<L>(l, 4 * i)) = float4{0.f, 0.f, 0.f, 0.f};
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  bool twice = false;
+  for (int j = 0; j < p.k - 1; ++j) {
+    const int other = __shfl(id, base + j, 64);     // (by all lanes: the source takes part)
+    twice = twice || (l > j && id >= 0 && id == other);
+  }
+  if (!__ballot(twice)) {
+    if (id >= 0) mine[id] = u;
+  } else {
+    for (int j = 0; j < p.k; ++j) {
+      if (l == j && id >= 0) mine[id] += u;
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
   }
-  for (int j = 0; j < p.k; ++j) {
-    const int ej = __shfl(id, base + j, 64) - e0;
-    const float uj = __shfl(u, base + j, 64);
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (ej == v) d[v] += uj;
-  }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   if (!in) return;
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    if (e0 + v >= p.E) continue;
-    const float o = routed ? d[v] : 0.f;
-    if constexpr (BF16) static_cast<uint16_t*>(p.dx)[size_t(t) * p.E + e0 + v] = uint16_t(bf16_bits(o));
-    else static_cast<float*>(p.dx)[size_t(t) * p.E + e0 + v] = o;
+  for (int i = 0; i < V / 4; ++i) {
+    const int e = expert_of<L>(l, 4 * i);
+    if (e >= p.E) continue;
+    const float4 w = *reinterpret_cast<const float4*>(mine + e);
+    float d[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      if (all) d[c] += pe[4 * i + c] * (f[4 * i + c] - off) * rest[4 * i + c];
+      if (!routed) d[c] = 0.f;
+    }
+    if (whole) {
+      if constexpr (BF16)
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.dx) + row + e) =
+            uint2{pack_bf16x2(d[0], d[1]), pack_bf16x2(d[2], d[3])};
+      else *reinterpret_cast<float4*>(static_cast<float*>(p.dx) + row + e) = float4{d[0], d[1], d[2], d[3]};
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (e + c >= p.E) continue;
+        if constexpr (BF16) static_cast<uint16_t*>(p.dx)[row + e + c] = uint16_t(bf16_bits(d[c]));
+        else static_cast<float*>(p.dx)[row + e + c] = d[c];
+      }
+    }
   }
 }
 

@@ -34,7 +34,7 @@ SHARED = [(dict(dt=2), INVALID), (dict(T=-1), INVALID), (dict(T=BIG), INVALID), 
 
 @pytest.mark.parametrize("kw,want", SHARED + [
     (dict(w=None), INVALID), (dict(bias=P + 2), INVALID), (dict(sums=None), INVALID), (dict(loss=None), INVALID),
-    (dict(loss=P + 2), INVALID), (dict(ws=None), INVALID), (dict(ws=P + 2), INVALID)])
+    (dict(loss=P + 2), INVALID), (dict(ws=None), INVALID), (dict(ws=P + 4), INVALID)])
 def test_route_validation(kw, want):
     assert call(dg.dg_moe_route, ROUTE, kw) == want
 
