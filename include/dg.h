@@ -552,7 +552,8 @@ typedef enum {
  *                 dg_moe_permute_fp8 (the A operand of the products with sa_rows =
  *                 1); null: none.  H a multiple of 16 (DG_ERR_UNSUPPORTED).
  *
- * N is that of the sum before its rounding to r_dtype.  Sums are held in 64 bits.
+ * N is that of the sum before its rounding to r_dtype.  Rows whose squares leave
+ * FP32's range have their sums in 64 bits.
  * Any H from 1 to 2^22 (above: DG_ERR_UNSUPPORTED); all matrices and w_post, w_pre
  * and a channel's gate are 16-byte aligned.  eps > 0; eps and alpha finite
  * (DG_ERR_INVALID_ARG).  T == 0 is a no-op.

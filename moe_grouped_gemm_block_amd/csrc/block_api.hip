@@ -40,9 +40,9 @@ DG_BLOCK_KERNEL(dg_moe_route_finish, kFinishExperts * kFinishParts, RouteArgs, r
 
 // (templates: stream and value types, codes, whole rows, wide rows)
 template <bool RB, bool YB, int CODES, bool WHOLE, bool WIDE>
-DG_BLOCK_KERNEL(dg_residual_norm_kernel, kNormMaxThreads, NormArgs, norm_body<RB, YB, CODES, WHOLE, WIDE>)
+DG_BLOCK_KERNEL(dg_residual_norm_kernel, WIDE ? kNormWideThreads : kNormMaxThreads, NormArgs, norm_body<RB, YB, CODES, WHOLE, WIDE>)
 template <bool RB, bool YB, bool WHOLE, bool WIDE>
-DG_BLOCK_KERNEL(dg_residual_norm_bwd_kernel, kNormMaxThreads, NormBwdArgs, norm_bwd_body<RB, YB, WHOLE, WIDE>)
+DG_BLOCK_KERNEL(dg_residual_norm_bwd_kernel, WIDE || (!WHOLE && !(RB && YB)) ? kNormWideThreads : kNormMaxThreads, NormBwdArgs, norm_bwd_body<RB, YB, WHOLE, WIDE>)
 DG_BLOCK_KERNEL(dg_residual_norm_columns, 1024, NormColumnsArgs, norm_columns_body)
 
 DG_BLOCK_KERNEL(dg_grad_squares, kClipThreads, ClipBatch, clip_squares_body)
@@ -84,14 +84,25 @@ bool valid_scores(int score, int renormalise, float scale) {
 
 // ---- norms -------------------------------------------------------------------------
 
-int norm_threads(int64_t H) {
-  return int(std::min<int64_t>(ceil_div(ceil_div(H, dg::kNormColumns), 64) * 64, dg::kNormMaxThreads));
+// Threads of a row that fits `most` threads' registers, or of a wider one.
+int norm_threads(int64_t H, int64_t most = dg::kNormMaxThreads) {
+  const int64_t threads = ceil_div(ceil_div(H, dg::kNormColumns), 64) * 64;
+  return int(threads <= most ? threads : dg::kNormWideThreads);
 }
+bool norm_wide(int64_t H, int64_t most = dg::kNormMaxThreads) { return H > dg::kNormColumns * most; }
+
+// The backward pass of FP32 rows that start at any element takes more registers.
+int64_t norm_bwd_most(int64_t H, bool bf16) { return H % 8 == 0 || bf16 ? dg::kNormMaxThreads : dg::kNormWideThreads; }
+
+// Rows that a workgroup of the backward pass takes at a time: as many as 8 waves hold.
+// (Fewer waves a workgroup would leave CUs without work to hide latency behind, more
+// workgroups would write more partial sums: 8192 rows of 512 28 us one at a time, 15 so.)
+int norm_bwd_groups(int64_t H) { return std::max(1, dg::kNormGroupThreads / norm_threads(H)); }
 
 int64_t norm_bwd_blocks(int64_t T, int64_t H) {
   // (partial sums of 16 MB at most for wide rows)
-  const int64_t most = H <= dg::kNormRegisterWidth ? 512 : std::max<int64_t>(1, (int64_t(1) << 22) / H);
-  return std::min(T, std::min<int64_t>(most, 512));
+  const int64_t most = norm_wide(H) ? std::max<int64_t>(1, (int64_t(1) << 22) / H) : 512;
+  return std::min(ceil_div(T, norm_bwd_groups(H)), std::min<int64_t>(most, 512));
 }
 
 int check_norm(int r_dtype, int dtype, const void* Y, const float* w_post, const float* gate, int gate_kind,
@@ -291,15 +302,17 @@ int dg_residual_norm(const void* R, int r_dtype, const void* Y, int dtype, const
   if (R_out && (R_out == R || R_out == Y)) return DG_ERR_INVALID_ARG;
   if (N && (N == R || N == Y)) return DG_ERR_INVALID_ARG;
   if (H > kMaxWidth || (Q && H % 16 != 0)) return DG_ERR_UNSUPPORTED;
-  const bool wide = H > dg::kNormRegisterWidth, whole = H % 8 == 0;
+  const bool wide = norm_wide(H), whole = H % 8 == 0;
   const int threads = norm_threads(H);
-  dg::NormArgs a{R, Y, w_post, gate, w_pre, R_out, N, static_cast<uint8_t*>(Q), S, eps, alpha, int(T), int(H),
+  dg::NormArgs a{R, Y, w_post, gate, w_pre, R_out, N, static_cast<uint8_t*>(Q), S, eps, 1.0 / double(H), alpha, int(T), int(H),
                  int(ceil_div(H, 128)), gate_kind};
   const int codes = !Q ? dg::kCodesNone : scale_mode == DG_SCALE_POW2 ? dg::kCodesPow2 : dg::kCodesAmax;
   const bool rb = r_dtype == DG_IN_BF16, yb = dtype == DG_IN_BF16;
   const auto kernel = rb ? (yb ? norm_kernel<true, true>(codes, whole, wide) : norm_kernel<true, false>(codes, whole, wide))
                          : (yb ? norm_kernel<false, true>(codes, whole, wide) : norm_kernel<false, false>(codes, whole, wide));
-  return launch(kernel, a, std::min<int64_t>(T, 256 * (2048 / threads)), threads, stream);
+  // three workgroups of 8 waves a CU are there at a time (8192 rows of 4096: 2 a CU 48.5, 3
+  // 47.5, 4 51 us)
+  return launch(kernel, a, std::min<int64_t>(T, 256 * std::max(1, 24 / (threads / 64))), threads, stream);
 }
 
 int64_t dg_residual_norm_bwd_workspace(int64_t T, int64_t H, int sums) {
@@ -330,13 +343,16 @@ int dg_residual_norm_bwd(const void* dR, const void* dN, const void* R, int r_dt
     if (dR_out == dR || dR_out == R || dR_out == dN || dR_out == Y || dR_out == dY) return DG_ERR_INVALID_ARG;
     if (dY && (dY == Y || dY == R || dY == dR || dY == dN)) return DG_ERR_INVALID_ARG;
     if ((pre || post) && bad(workspace, 16)) return DG_ERR_INVALID_ARG;
-    const bool wide = H > dg::kNormRegisterWidth, whole = H % 8 == 0;
+    const bool rb = r_dtype == DG_IN_BF16, yb = dtype == DG_IN_BF16, whole = H % 8 == 0;
+    const int64_t most = norm_bwd_most(H, rb && yb);
+    const bool wide = norm_wide(H, most);
+    const int threads = norm_threads(H, most);
     dg::NormBwdArgs a{dR, dN, pre ? R : nullptr, Y, w_post, gate, w_pre, dR_out, dY, token ? dgate : nullptr,
-                      part_pre, part_post, eps, alpha, int(T), int(H), gate_kind};
-    const bool rb = r_dtype == DG_IN_BF16, yb = dtype == DG_IN_BF16;
+                      part_pre, part_post, eps, 1.0 / double(H), alpha, int(T), int(H), gate_kind,
+                      threads / 64};
     const auto kernel = rb ? (yb ? norm_bwd_kernel<true, true>(whole, wide) : norm_bwd_kernel<true, false>(whole, wide))
                            : (yb ? norm_bwd_kernel<false, true>(whole, wide) : norm_bwd_kernel<false, false>(whole, wide));
-    const int st1 = launch(kernel, a, nb, norm_threads(H), stream);
+    const int st1 = launch(kernel, a, nb, threads * norm_bwd_groups(H), stream);
     if (st1 != DG_OK) return st1;
   }
   if (!pre && !post) return DG_OK;

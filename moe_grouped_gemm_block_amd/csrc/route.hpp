@@ -455,10 +455,20 @@ __device__ __forceinline__ void route_finish_body(const RouteArgs& p) {
   float sum = 0.f;
   int count = 0;
   if (e < p.E) {
-#pragma unroll 8
-    for (int b = part; b < p.nb; b += kFinishParts) {
-      sum += p.part_sums[size_t(b) * p.E + e];
-      count += p.part_counts[size_t(b) * p.E + e];
+    // (at most kRouteMaxBlocks: all loads on their way at once)
+    constexpr int N = kRouteMaxBlocks / kFinishParts;
+    float s[N];
+    int32_t c[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int b = part + i * kFinishParts;
+      s[i] = b < p.nb ? p.part_sums[size_t(b) * p.E + e] : 0.f;
+      c[i] = b < p.nb ? p.part_counts[size_t(b) * p.E + e] : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      sum += s[i];
+      count += c[i];
     }
   }
   sums[part][col] = sum;
