@@ -310,9 +310,9 @@ int dg_residual_norm(const void* R, int r_dtype, const void* Y, int dtype, const
   const bool rb = r_dtype == DG_IN_BF16, yb = dtype == DG_IN_BF16;
   const auto kernel = rb ? (yb ? norm_kernel<true, true>(codes, whole, wide) : norm_kernel<true, false>(codes, whole, wide))
                          : (yb ? norm_kernel<false, true>(codes, whole, wide) : norm_kernel<false, false>(codes, whole, wide));
-  // three workgroups of 8 waves a CU are there at a time (8192 rows of 4096: 2 a CU 48.5, 3
-  // 47.5, 4 51 us)
-  return launch(kernel, a, std::min<int64_t>(T, 256 * std::max(1, 24 / (threads / 64))), threads, stream);
+  // as many workgroups as are there at a time by their registers, three of 8 waves a CU, for
+  // codes two (8192 rows of 4096: 2 a CU 48.5, 3 47.5, 4 51 us; codes 2 76, 3 78)
+  return launch(kernel, a, std::min<int64_t>(T, 256 * std::max(1, (Q ? 16 : 24) / (threads / 64))), threads, stream);
 }
 
 int64_t dg_residual_norm_bwd_workspace(int64_t T, int64_t H, int sums) {

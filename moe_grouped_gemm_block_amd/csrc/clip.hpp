@@ -56,6 +56,7 @@ __device__ __forceinline__ double chunk_squares(const ClipTensor& x, int64_t beg
   int done = 0;
   if (x.whole) {
     done = n / V * V;
+#pragma unroll 4
     for (int i = threadIdx.x * V; i < done; i += kClipThreads * V) {
       float v[V];
       load_values<BF16, V>(x.g, size_t(begin) + i, v);
@@ -110,15 +111,27 @@ template <bool IN, bool OUT>
 __device__ __forceinline__ void chunk_scaled(const ClipTensor& x, int64_t begin, int n, float f) {
   int done = 0;
   if (x.whole) {
-    done = n / 8 * 8;
-    for (int i = threadIdx.x * 8; i < done; i += kClipThreads * 8) {
-      float v[8];
-      load_values<IN, IN ? 8 : 4>(x.g, size_t(begin) + i, v);
-      if constexpr (!IN) load_values<IN, 4>(x.g, size_t(begin) + i + 4, v + 4);
+    // pieces of 16 bytes of the wider type, so that a wave's stores are of whole lines
+    constexpr int V = IN && OUT ? 8 : 4;
+    done = n / V * V;
+#pragma unroll 4
+    for (int i = threadIdx.x * V; i < done; i += kClipThreads * V) {
+      float v[V];
+      if constexpr (IN && !OUT) {
+        const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(x.g) + begin + i);
+        v[0] = __uint_as_float(w.x << 16);
+        v[1] = __uint_as_float(w.x & 0xFFFF0000u);
+        v[2] = __uint_as_float(w.y << 16);
+        v[3] = __uint_as_float(w.y & 0xFFFF0000u);
+      } else {
+        load_values<IN, V>(x.g, size_t(begin) + i, v);
+      }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] *= f;
-      store_values<OUT, OUT ? 8 : 4>(x.out, size_t(begin) + i, v);
-      if constexpr (!OUT) store_values<OUT, 4>(x.out, size_t(begin) + i + 4, v + 4);
+      for (int k = 0; k < V; ++k) v[k] *= f;
+      if constexpr (!IN && OUT)
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(x.out) + begin + i) = uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+      else
+        store_values<OUT, V>(x.out, size_t(begin) + i, v);
     }
   }
   for (int i = done + threadIdx.x; i < n; i += kClipThreads) {

@@ -240,39 +240,54 @@ struct NormArgs {
   int T, H, Kb, gate_kind;
 };
 
-// The next float towards zero, its last bit set if v is no float: rounding that to
-// fewer bits is rounding v itself.
-__device__ __forceinline__ float round_odd(double v) {
-  const float f = float(v);
-  uint32_t b = __float_as_uint(f);
-  if (double(f) != v) {
-    b -= __builtin_fabs(double(f)) > __builtin_fabs(v);
-    b |= 1u;
-  }
-  return __uint_as_float(b);
-}
-
-// Codes of eight values n of a block that 16 lanes share, and its scale.
+// Codes of eight values n (f: the same as FP32) of a block that 16 lanes share, and its
+// scale.  The codes are those of n / s rounded once: FP32 quotients at both ends of a
+// bracket of +-2^-20 around n / s (f is within 2^-24 of n, the reciprocal within 2^-22)
+// agree about it but for one value in 2^16, which is then divided in 64 bits.  (All
+// quotients in 64 bits: 8192 rows of 4096 in BF16 to codes 81 us, so 76; the rest of that is
+// the 64-bit arithmetic before.)
 template <bool POW2>
-__device__ __forceinline__ uint2 encode8(const double (&n)[8], float& s) {
-  double amax = 0.0;
+__device__ __forceinline__ uint2 encode8(const double (&n)[8], const float (&f)[8], float& s) {
+  auto amax64 = [&] {
+    double a = 0.0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) amax = fmax(amax, __builtin_fabs(n[i]));
-  amax = group_max<16>(amax);
-  s = 1.f;
-  if (amax > 0.0) {
-    if constexpr (POW2) {
-      const int e = __builtin_amdgcn_frexp_exp(amax) - (__builtin_amdgcn_frexp_mant(amax) > 0.875 ? 8 : 9);
-      s = pow2f(min(max(e, -126), 126));
-    } else {
-      s = float(amax / 448.0);
+    for (int i = 0; i < 8; ++i) a = fmax(a, __builtin_fabs(n[i]));
+    return group_max<16>(a);
+  };
+  float amax = 0.f, r;
+  if constexpr (POW2) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, __builtin_fabsf(f[i]));
+    amax = group_max<16>(amax);
+    int e = pow2_exponent(amax);
+    if (__builtin_expect(e != pow2_exponent(amax * (1.f + 0x1p-20f)) || e != pow2_exponent(amax * (1.f - 0x1p-20f)), 0)) {
+      const double a = amax64();
+      e = max(__builtin_amdgcn_frexp_exp(a) - (__builtin_amdgcn_frexp_mant(a) > 0.875 ? 8 : 9), -126);
+    }
+    e = amax > 0.f ? min(e, 126) : 0;
+    s = pow2f(e);
+    r = pow2f(-e);
+  } else {
+    const double a = amax64();
+    s = a > 0.0 ? float(a / 448.0) : 1.f;
+    r = __builtin_amdgcn_rcpf(s);
+  }
+  const bool far = !(s >= 0x1p-100f);
+  const float r_lo = r * (1.f - 0x1p-20f), r_hi = r * (1.f + 0x1p-20f);
+  uint32_t w[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    w[j] = hw_codes4(f[4 * j] * r_lo, f[4 * j + 1] * r_lo, f[4 * j + 2] * r_lo, f[4 * j + 3] * r_lo);
+    const uint32_t hi = hw_codes4(f[4 * j] * r_hi, f[4 * j + 1] * r_hi, f[4 * j + 2] * r_hi, f[4 * j + 3] * r_hi);
+    if (__builtin_expect(w[j] != hi || far, 0)) {
+      uint32_t c = 0;
+#pragma unroll 1
+      for (int i = 0; i < 4; ++i)
+        c |= e4m3_of_f64(eight_at(n, 4 * j + i, std::make_integer_sequence<int, 8>{}) / double(s)) << (8 * i);
+      w[j] = c;
     }
   }
-  const double r = s > 0.f ? 1.0 / double(s) : 0.0;
-  float v[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = __builtin_amdgcn_fmed3f(round_odd(n[i] * r), -448.f, 448.f);
-  return uint2{hw_codes4(v[0], v[1], v[2], v[3]), hw_codes4(v[4], v[5], v[6], v[7])};
+  return uint2{w[0], w[1]};
 }
 
 // RB, YB: the stream and the block's output (and n) are BF16, else FP32.  WIDE: rows
@@ -363,7 +378,7 @@ __device__ __forceinline__ void norm_body(const NormArgs& p) {
       for (int i = 0; i < 8; ++i) {
         v[i] = r[i];
         if constexpr (CODES != kCodesNone) {
-          if (block) v[i] += (y[i] * by) * onto64[i];
+          if (block) v[i] = __builtin_fma(y[i] * by, onto64[i], v[i]);
         } else {
           if (block) v[i] = __builtin_fmaf(y[i] * by, onto[i], v[i]);
         }
@@ -392,15 +407,13 @@ __device__ __forceinline__ void norm_body(const NormArgs& p) {
       F n[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) n[i] = c < p.H ? (v[i] * pre) * w_pre[i] : F(0);
-      if (p.N) {
-        float o[8];
+      float o[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = float(n[i]);
-        store8<YB, WHOLE>(p.N, row, c, p.H, o);
-      }
+      for (int i = 0; i < 8; ++i) o[i] = float(n[i]);
+      if (p.N) store8<YB, WHOLE>(p.N, row, c, p.H, o);
       if constexpr (CODES != kCodesNone) {
         float s;
-        const uint2 q = encode8<CODES == kCodesPow2>(n, s);
+        const uint2 q = encode8<CODES == kCodesPow2>(n, o, s);
         if (c < p.H) {
           *reinterpret_cast<uint2*>(p.Q + row + c) = q;
           if ((threadIdx.x & 15) == 0) p.S[size_t(t) * p.Kb + c / 128] = s;
