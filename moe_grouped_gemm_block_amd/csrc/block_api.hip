@@ -47,6 +47,7 @@ DG_BLOCK_KERNEL(dg_residual_norm_columns, 1024, NormColumnsArgs, norm_columns_bo
 
 DG_BLOCK_KERNEL(dg_grad_squares, kClipThreads, ClipBatch, clip_squares_body)
 DG_BLOCK_KERNEL(dg_grad_norm_sum, kClipNormThreads, ClipNormArgs, clip_norm_body)
+DG_BLOCK_KERNEL(dg_grad_norm_few, kClipNormThreads, ClipBatch, clip_norm_few_body)
 DG_BLOCK_KERNEL(dg_clip_scale, kClipThreads, ClipBatch, clip_scale_body)
 #undef DG_BLOCK_KERNEL
 
@@ -198,16 +199,29 @@ int clip_disjoint(const void* const* grads, const int64_t* sizes, const int* dty
   return 1;
 }
 
+// Whether one workgroup takes the norm (below 2 us, where two launches take 4; at
+// kClipFew elements both take about 5).
+bool clip_few(const int64_t* sizes, int count) {
+  int64_t n = 0;
+  int tensors = 0;
+  for (int i = 0; i < count; ++i) {
+    n += sizes[i];
+    tensors += sizes[i] > 0;
+    if (n > dg::kClipFew || tensors > dg::kClipTensors) return false;
+  }
+  return true;
+}
+
 // The launches of a kernel over a list, up to kClipTensors tensors that are not empty
 // each; `fill` completes a tensor's entry.
 template <typename F>
 int clip_launches(void (*kernel)(dg::ClipBatch), dg::ClipBatch& b, const void* const* grads, const int64_t* sizes,
-                  const int* dtypes, int count, hipStream_t stream, F fill) {
+                  const int* dtypes, int count, hipStream_t stream, F fill, bool few = false) {
   b.count = b.chunks = 0;
   for (int i = 0; i <= count; ++i) {
     const int64_t chunks = i < count ? ceil_div(sizes[i], dg::kClipChunk) : 0;
     if (b.count == dg::kClipTensors || (i == count && b.count > 0)) {
-      const int st = launch(kernel, b, b.chunks, dg::kClipThreads, stream);
+      const int st = launch(kernel, b, few ? 1 : b.chunks, few ? dg::kClipNormThreads : dg::kClipThreads, stream);
       if (st != DG_OK) return st;
       if (b.part) b.part += b.chunks;
       b.count = b.chunks = 0;
@@ -365,17 +379,23 @@ int dg_residual_norm_bwd(const void* dR, const void* dN, const void* R, int r_dt
 
 int64_t dg_grad_norm_workspace(const int64_t* sizes, const int* dtypes, int count) {
   const int64_t chunks = clip_chunks(sizes, dtypes, count);
-  return chunks < 0 ? chunks : 8 * chunks;
+  return chunks < 0 ? chunks : clip_few(sizes, count) ? 0 : 8 * chunks;
 }
 
 int dg_grad_norm(const void* const* grads, const int64_t* sizes, const int* dtypes, int count, float* norm,
                  void* workspace, hipStream_t stream) {
   const int64_t chunks = clip_chunks(sizes, dtypes, count);
   if (chunks < 0) return int(chunks);
-  if (bad(norm, 4) || (chunks > 0 && (grads == nullptr || bad(workspace, 8)))) return DG_ERR_INVALID_ARG;
+  if (bad(norm, 4) || (chunks > 0 && grads == nullptr)) return DG_ERR_INVALID_ARG;
+  const bool few = clip_few(sizes, count);
+  if (!few && bad(workspace, 8)) return DG_ERR_INVALID_ARG;
   for (int i = 0; i < count; ++i)
     if (sizes[i] > 0 && bad(grads[i], elem(dtypes[i]))) return DG_ERR_INVALID_ARG;
   dg::ClipBatch b{};
+  if (few && chunks > 0) {
+    b.norm_out = norm;
+    return clip_launches(dg::dg_grad_norm_few, b, grads, sizes, dtypes, count, stream, [](dg::ClipTensor&, int) {}, true);
+  }
   b.part = static_cast<double*>(workspace);
   const int st = clip_launches(dg::dg_grad_squares, b, grads, sizes, dtypes, count, stream, [](dg::ClipTensor&, int) {});
   if (st != DG_OK) return st;

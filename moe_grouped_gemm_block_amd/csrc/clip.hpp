@@ -35,7 +35,8 @@ struct ClipBatch {
   ClipTensor t[kClipTensors];
   int count, chunks;
   double* part;              // [chunks], this launch's
-  const float* norm;
+  const float* norm;         // clipping
+  float* norm_out;           // the norm of few elements
   float max_norm;
 };
 static_assert(sizeof(ClipBatch) <= 4096, "arguments of a launch");
@@ -49,22 +50,23 @@ __device__ __forceinline__ int clip_tensor(const ClipBatch& p, int chunk) {
   return lo;
 }
 
+// A thread's share of the squares of a chunk's n elements, kClipThreads threads together.
 template <bool BF16>
-__device__ __forceinline__ double chunk_squares(const ClipTensor& x, int64_t begin, int n) {
+__device__ __forceinline__ double chunk_squares(const ClipTensor& x, int64_t begin, int n, int thread) {
   constexpr int V = BF16 ? 8 : 4;
   double sum = 0.0;
   int done = 0;
   if (x.whole) {
     done = n / V * V;
 #pragma unroll 4
-    for (int i = threadIdx.x * V; i < done; i += kClipThreads * V) {
+    for (int i = thread * V; i < done; i += kClipThreads * V) {
       float v[V];
       load_values<BF16, V>(x.g, size_t(begin) + i, v);
 #pragma unroll
       for (int k = 0; k < V; ++k) sum += double(v[k]) * v[k];
     }
   }
-  for (int i = done + threadIdx.x; i < n; i += kClipThreads) {
+  for (int i = done + thread; i < n; i += kClipThreads) {
     float v;
     load_values<BF16, 1>(x.g, size_t(begin) + i, &v);
     sum += double(v) * v;
@@ -72,15 +74,19 @@ __device__ __forceinline__ double chunk_squares(const ClipTensor& x, int64_t beg
   return sum;
 }
 
+// A wave's sum of a chunk's squares.
+__device__ __forceinline__ double wave_squares(const ClipBatch& p, int chunk, int thread) {
+  const ClipTensor& x = p.t[clip_tensor(p, chunk)];
+  const int64_t begin = int64_t(chunk - x.first) * kClipChunk;
+  const int n = int(min(x.n - begin, int64_t(kClipChunk)));
+  return group_sum<64>(x.bf16 ? chunk_squares<true>(x, begin, n, thread) : chunk_squares<false>(x, begin, n, thread));
+}
+
 __device__ __forceinline__ void clip_squares_body(const ClipBatch& p) {
   __shared__ double sums[kClipThreads / 64];
   const int chunk = block_index();
   if (chunk >= p.chunks) return;
-  const ClipTensor& x = p.t[clip_tensor(p, chunk)];
-  const int64_t begin = int64_t(chunk - x.first) * kClipChunk;
-  const int n = int(min(x.n - begin, int64_t(kClipChunk)));
-  double s = x.bf16 ? chunk_squares<true>(x, begin, n) : chunk_squares<false>(x, begin, n);
-  s = group_sum<64>(s);
+  const double s = wave_squares(p, chunk, threadIdx.x);
   if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = s;
   __syncthreads();
   if (threadIdx.x == 0) p.part[chunk] = (sums[0] + sums[1]) + (sums[2] + sums[3]);
@@ -94,17 +100,38 @@ struct ClipNormArgs {
 
 constexpr int kClipNormThreads = 1024;
 
-__device__ __forceinline__ void clip_norm_body(const ClipNormArgs& p) {
+__device__ __forceinline__ void clip_norm_of(double s, float* norm) {
   __shared__ double sums[kClipNormThreads / 64];
-  double s = 0.0;
-  for (int64_t i = threadIdx.x; i < p.n; i += kClipNormThreads) s += p.part[i];
   s = group_sum<64>(s);
   if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = s;
   __syncthreads();
   if (threadIdx.x == 0) {
     for (int w = 1; w < kClipNormThreads / 64; ++w) s += sums[w];
-    *p.norm = float(sqrt(s));
+    *norm = float(sqrt(s));
   }
+}
+
+__device__ __forceinline__ void clip_norm_body(const ClipNormArgs& p) {
+  double s = 0.0;
+  // (eight loads on their way at a time)
+  for (int64_t i0 = threadIdx.x; i0 < p.n; i0 += 8 * kClipNormThreads) {
+    double v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = i0 + k * kClipNormThreads < p.n ? p.part[i0 + k * kClipNormThreads] : 0.0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s += v[k];
+  }
+  clip_norm_of(s, p.norm);
+}
+
+// Few elements: one workgroup squares and sums in one launch, four chunks at a time.
+constexpr int64_t kClipFew = 65536;
+
+__device__ __forceinline__ void clip_norm_few_body(const ClipBatch& p) {
+  double s = 0.0;
+  for (int chunk = threadIdx.x / kClipThreads; chunk < p.chunks; chunk += kClipNormThreads / kClipThreads)
+    s += wave_squares(p, chunk, threadIdx.x % kClipThreads);
+  clip_norm_of((threadIdx.x & 63) == 0 ? s : 0.0, p.norm_out);
 }
 
 template <bool IN, bool OUT>
@@ -149,9 +176,11 @@ __device__ __forceinline__ float clip_factor(float norm, float max_norm) {
   return f >= 1.0 ? 1.f : float(f);
 }
 
+// Chunks from the last on: what the norm read last is still in the caches (201 M BF16
+// into FP32 191 us, from the first on 215).
 __device__ __forceinline__ void clip_scale_body(const ClipBatch& p) {
-  const int chunk = block_index();
-  if (chunk >= p.chunks) return;
+  const int chunk = p.chunks - 1 - int(block_index());
+  if (chunk < 0) return;
   const float f = clip_factor(*p.norm, p.max_norm);
   const ClipTensor& x = p.t[clip_tensor(p, chunk)];
   if (f == 1.f && x.g == x.out) return;         // in place, and nothing to change

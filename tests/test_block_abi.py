@@ -119,7 +119,8 @@ def clip_of(tensors, outs, norm=P, max_norm=1.0):
 def test_grad_norm_validation():
     one = [(P, 10, 0)]
     assert norm_of(one, norm=None) == INVALID and norm_of(one, norm=P + 2) == INVALID
-    assert norm_of(one, ws=None) == INVALID and norm_of(one, ws=P + 4) == INVALID
+    large = [(P, 100000, 0)]
+    assert norm_of(large, ws=None) == INVALID and norm_of(large, ws=P + 4) == INVALID
     for t in [(None, 10, 0), (P + 2, 10, 0), (P + 1, 10, 1), (P, -1, 0), (P, 10, 2), (P, 1 << 46, 0)]:
         assert norm_of([t]) == INVALID, t
     assert dg.dg_grad_norm(None, None, None, 1, P, P, None) == INVALID
