@@ -524,7 +524,7 @@ int dg_moe_route(const void* logits, int dtype, const float* bias, const uint8_t
  * float32 [1], the gradient of the loss.  Choices and counts are constants; counts
  * and routed may be those of several devices added up.  counts, routed and dloss are
  * all null where the loss takes no part.  ids outside [0, E) are no choices (their
- * dweights are not used); a row without choices gives zeros, its logits are not read.
+ * dweights are not used); a row without choices gives zeros, whatever its logits are.
  */
 int dg_moe_route_bwd(const float* dweights, const void* logits, int dtype, const int32_t* ids,
                      const int32_t* counts, const int32_t* routed, const float* dloss, int64_t T, int64_t E,

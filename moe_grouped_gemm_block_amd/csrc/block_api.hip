@@ -291,7 +291,7 @@ int dg_moe_route_bwd(const float* dweights, const void* logits, int dtype, const
   if (T == 0) return DG_OK;
   if (bad(dweights, 4) || bad(logits, 16) || bad(ids, 4) || bad(dlogits, 16)) return DG_ERR_INVALID_ARG;
   dg::RouteBwdArgs a{logits, ids, dweights, counts, routed, dloss, dlogits, int(T), int(E), top_k,
-                     score == DG_SCORE_SIGMOID, renormalise, scale};
+                     score == DG_SCORE_SIGMOID, renormalise, aligned(counts, 16), scale};
 #define DG_ROUTE_TABLE(T)                                                                                       \
   {dg::dg_moe_route_bwd_##T##_16x4, dg::dg_moe_route_bwd_##T##_16x16, dg::dg_moe_route_bwd_##T##_64x4,          \
    dg::dg_moe_route_bwd_##T##_64x16}

@@ -17,12 +17,11 @@ template <int ROR, typename T>
 __device__ __forceinline__ T row_rotated(T v) {
   constexpr int CTRL = 0x120 + ROR;
   if constexpr (sizeof(T) == 4) {
-    const int b = __builtin_bit_cast(int, v);
-    return __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(b, b, CTRL, 0xF, 0xF, false));
+    return __builtin_bit_cast(T, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
   } else {
     const int2 b = __builtin_bit_cast(int2, v);
-    return __builtin_bit_cast(T, make_int2(__builtin_amdgcn_update_dpp(b.x, b.x, CTRL, 0xF, 0xF, false),
-                                           __builtin_amdgcn_update_dpp(b.y, b.y, CTRL, 0xF, 0xF, false)));
+    return __builtin_bit_cast(T, make_int2(__builtin_amdgcn_mov_dpp(b.x, CTRL, 0xF, 0xF, true),
+                                           __builtin_amdgcn_mov_dpp(b.y, CTRL, 0xF, 0xF, true)));
   }
 }
 
@@ -58,14 +57,6 @@ __device__ __forceinline__ T group_reduce(T v, F f) {
     v = across<32>(v, f);
   }
   return v;
-}
-
-// v of lane I of the row of 16
-template <int I, typename T>
-__device__ __forceinline__ T row_broadcast(T v) {
-  static_assert(sizeof(T) == 4, "one register");
-  const int b = __builtin_bit_cast(int, v);
-  return __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(b, b, 0x150 + I, 0xF, 0xF, false));
 }
 
 template <int L, typename T>

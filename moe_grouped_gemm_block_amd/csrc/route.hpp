@@ -78,17 +78,50 @@ __device__ __forceinline__ float shifted_score(float x, float m, bool sigmoid) {
   return num * __builtin_amdgcn_rcpf(1.f + a);
 }
 
+// The same for V logits, and with REST what one_minus_sigmoid gives (1 for softmax).
+// The branches are the wave's, not an element's: with one at each element its exponential
+// waits for the one before.
+template <bool REST, int V>
+__device__ __forceinline__ void shifted_scores(const float (&x)[V], float m, bool sigmoid, float (&s)[V], float (&rest)[REST ? V : 1]) {
+  if (!sigmoid) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      s[v] = exp_nonpos(x[v] - m);
+      if constexpr (REST) rest[v] = 1.f;
+    }
+    return;
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const float a = exp_nonpos(-__builtin_fabsf(x[v])), r = __builtin_amdgcn_rcpf(1.f + a);
+    const bool up = x[v] > 0.f;
+    s[v] = (up ? 1.f : a) * r;
+    if constexpr (REST) rest[v] = (up ? a : 1.f) * r;
+  }
+  if (__ballot(m < 0.f)) {                          // tokens whose scores may underflow
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float r = __builtin_amdgcn_rcpf(1.f + exp_nonpos(-__builtin_fabsf(x[v])));
+      s[v] = m < 0.f ? exp_nonpos(x[v] - m) * r : s[v];
+    }
+  }
+}
+
 // 1 - 1 / (1 + e^-x) without cancellation
 __device__ __forceinline__ float one_minus_sigmoid(float x) {
   const float a = exp_nonpos(-__builtin_fabsf(x));
   return (x > 0.f ? a : 1.f) * __builtin_amdgcn_rcpf(1.f + a);
 }
 
-// Unsigned integers in the order of the values: 0 for -inf, NaN last, -0 as 0.
+// Unsigned integers in the order of the values: 0 for -inf, from 1 on for numbers, NaN
+// last; -0 as 0.
+constexpr uint32_t kClosedKeys = 0x3FFu;          // room below the first number's key, see the choice
+constexpr uint32_t kNaNKey = 0xFFFFFFFFu - kClosedKeys;
 __device__ __forceinline__ uint32_t order_key(float x) {
   const uint32_t b = __float_as_uint(x + 0.f);
   const uint32_t key = b ^ (uint32_t(int32_t(b) >> 31) | 0x80000000u);
-  return x != x ? 0xFFFFFFFFu : x == -__builtin_inff() ? 0u : key;
+  // less what -inf has, 0x7FFFFF, but not below 0
+  return x != x ? kNaNKey : __builtin_elementwise_sub_sat(key, 0x7FFFFFu);
 }
 __device__ __forceinline__ uint64_t order_key(double x) {
   const uint64_t b = uint64_t(__double_as_longlong(x + 0.0));
@@ -96,6 +129,7 @@ __device__ __forceinline__ uint64_t order_key(double x) {
   return x != x ? ~uint64_t(0) : x == -__builtin_inf() ? 0u : key;
 }
 __device__ __forceinline__ float key_value(uint32_t key) {
+  key = key > 0xFF000001u ? 0xFFFFFFFFu : key + 0x7FFFFFu;         // (+inf has 0xFF000001)
   return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
 }
 
@@ -173,9 +207,11 @@ __device__ __forceinline__ T pick(const T (&a)[V], int i) {
 
 // ---- choice -----------------------------------------------------------------------
 // A value's order key with its lowest bits replaced by the expert's number, the lower
-// number larger: the largest of a group names its expert, and taking it out is one
-// comparison per register, where a search for the index beside whole keys takes another
-// 36 instructions a choice.  What the lost bits leave open is settled afterwards: the
+// number larger: the largest of a group names its expert, where a search for the index
+// beside whole keys takes another 36 instructions a choice.  No key is taken out: keys
+// minus the last one taken, as unsigned numbers, are in the same order, and those already
+// taken lie below all others (key - g < 2^32 - g from g on, and at least that, by wrapping
+// round, below it), so the next one is the largest again.  What the lost bits leave open is settled afterwards: the
 // choices go on past the k-th until one is certainly smaller than the one before, and
 // where two in a row were too close to tell, lane j computes the j-th one's whole key, and
 // they are ranked by those.  BF16 logits lose nothing.  Where more than a lane each are
@@ -192,10 +228,11 @@ __device__ __forceinline__ float biased_tolerance(float largest, float most, boo
 template <bool BF16, int L, int V, bool BIASED>
 __device__ __forceinline__ void route_body(const RouteArgs& p) {
   constexpr int PER_WAVE = 64 / L, PER_BLOCK = kRouteWaves * PER_WAVE;
+  static_assert(kRouteThreads % (L * V) == 0 && PER_BLOCK % (kRouteThreads / (L * V)) == 0, "threads share experts evenly");
   constexpr uint32_t NUMBER = L * V - 1;            // bits of an expert's number
   constexpr bool WHOLE_KEYS = BF16 && !BIASED;      // all of a key is above them
   __shared__ int32_t count[L * V];
-  __shared__ float part[kRouteWaves][L * V];        // lane l's v-th at v L + l: no bank conflicts
+  __shared__ __attribute__((aligned(16))) float part[PER_BLOCK][L * V];     // a group's sums of p
   __shared__ int routed_of[kRouteWaves];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int l = lane & (L - 1), base = lane & ~(L - 1);
@@ -203,7 +240,9 @@ __device__ __forceinline__ void route_body(const RouteArgs& p) {
   const float inf = __builtin_inff();
   if (balance) {
     for (int e = threadIdx.x; e < L * V; e += kRouteThreads) count[e] = 0;
-    for (int i = lane; i < L * V; i += 64) part[wave][i] = 0.f;     // (the wave's own)
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i)
+      *reinterpret_cast<float4*>(part[wave * PER_WAVE + lane / L] + expert_of<L>(l, 4 * i)) = float4{0.f, 0.f, 0.f, 0.f};
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.done = 0;
     __syncthreads();
   }
@@ -221,19 +260,22 @@ __device__ __forceinline__ void route_body(const RouteArgs& p) {
 #pragma unroll
       for (int v = 0; v < V; ++v) x[v] = -inf;
     }
-    uint32_t key[V];
-    uint32_t top = 0;
+    // (NaN where one of them is NaN)
+    float m = x[0];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      key[v] = order_key(x[v]);
-      top = max(top, key[v]);
+    for (int v = 1; v < V; ++v) m = __builtin_elementwise_maximum(m, x[v]);
+    m = group_reduce<L>(m, [](float a, float b) { return __builtin_elementwise_maximum(a, b); });
+    const bool open = m != -inf;
+    if (!open) m = 0.f;
+    uint32_t key[V];
+    if constexpr (!BIASED) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) key[v] = order_key(x[v]);
     }
-    top = group_max<L>(top);
-    const float m = top ? key_value(top) : 0.f;
 
     // scores of all experts (over e^min(m, 0) or e^m), where something needs them; they
     // are not kept in registers during the choice
-    bool routed = top != 0;
+    bool routed = open;
     float z = 1.f;
     [[maybe_unused]] float f = 1.f;                 // what makes them scores
     [[maybe_unused]] auto biased_keys = [&](const float (&s)[V]) {
@@ -243,15 +285,13 @@ __device__ __forceinline__ void route_body(const RouteArgs& p) {
       for (int v = 0; v < V; ++v) key[v] = x[v] == -inf ? 0u : order_key(__builtin_fmaf(s[v], f, bias[v]));
     };
     if (BIASED || balance || (!p.renorm && !sigmoid)) {
-      float s[V];
+      float s[V], none[1];
+      shifted_scores<false>(x, m, sigmoid, s, none);
       z = 0.f;
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        s[v] = shifted_score(x[v], m, sigmoid);
-        z += s[v];
-      }
+      for (int v = 0; v < V; ++v) z += s[v];
       z = group_sum<L>(z);
-      if (top == 0) z = 1.f;
+      if (!open) z = 1.f;
       const float r = 1.f / z;
       if constexpr (BIASED) {
         f = sigmoid ? exp_nonpos(fminf(m, 0.f)) : r;
@@ -263,35 +303,40 @@ __device__ __forceinline__ void route_body(const RouteArgs& p) {
       }
       if (balance) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-          float pe = routed ? s[v] * r : 0.f;
-          if constexpr (L == 16) {
-            pe = across<16>(pe, [](float a, float b) { return a + b; });
-            pe = across<32>(pe, [](float a, float b) { return a + b; });
-          }
-          if (lane < L) part[wave][v * L + l] += pe;
+        for (int i = 0; i < V / 4; ++i) {
+          float4* at = reinterpret_cast<float4*>(part[wave * PER_WAVE + lane / L] + expert_of<L>(l, 4 * i));
+          float4 sum = *at;
+          sum.x += routed ? s[4 * i] * r : 0.f;
+          sum.y += routed ? s[4 * i + 1] * r : 0.f;
+          sum.z += routed ? s[4 * i + 2] * r : 0.f;
+          sum.w += routed ? s[4 * i + 3] * r : 0.f;
+          *at = sum;
         }
       }
     }
 
     // lane j of the group takes choice j
     const float most = sigmoid ? 1.f : f;
+    // (moved up so that closed experts' keys, and no others, stay within kClosedKeys)
+    static_assert(NUMBER <= kClosedKeys, "numbers of closed experts");
 #pragma unroll
     for (int v = 0; v < V; ++v)
-      key[v] = key[v] ? (key[v] & ~NUMBER) | (NUMBER - uint32_t(expert_of<L>(l, v))) : 0u;
-    uint32_t mine = 0;
-    [[maybe_unused]] uint32_t before = 0;
+      key[v] = ((key[v] + kClosedKeys) & ~NUMBER) | (NUMBER - uint32_t(expert_of<L>(l, v)));
+    uint32_t mine = 0, last = 0;
     [[maybe_unused]] bool close = false, more = false;
+    bool left = true;                               // experts to choose from
     int n = p.k;                                    // choices that there are
     for (int j = 0; WHOLE_KEYS ? j < p.k : j <= L; ++j) {
       uint32_t best = 0;
 #pragma unroll
-      for (int v = 0; v < V; ++v) best = max(best, key[v]);
-      const uint32_t g = group_max<L>(best);
+      for (int v = 0; v < V; ++v) best = max(best, key[v] - last);
+      uint32_t g = group_max<L>(best) + last;
+      left = left && g > kClosedKeys;
+      if (!left) g = 0;
       if constexpr (!WHOLE_KEYS) {
         more = false;
-        if (j > 0 && g != 0) {
-          const uint32_t high = g | NUMBER, low = before & ~NUMBER;   // bounds of their keys
+        if (j > 0 && left) {
+          const uint32_t high = (g | NUMBER) - kClosedKeys, low = (last & ~NUMBER) - kClosedKeys;   // bounds of their keys
           if constexpr (BIASED) more = !(key_value(low) - key_value(high) > biased_tolerance(key_value(low), most, sigmoid));
           else more = high >= low;
         }
@@ -301,11 +346,9 @@ __device__ __forceinline__ void route_body(const RouteArgs& p) {
         }
         close = close || more;
         n = j;
-        before = g;
       }
       if (l == j) mine = g;
-#pragma unroll
-      for (int v = 0; v < V; ++v) key[v] = key[v] == g ? 0u : key[v];
+      last = g;
     }
     int id = mine ? int(NUMBER - (mine & NUMBER)) : -1;
 
@@ -345,9 +388,8 @@ __device__ __forceinline__ void route_body(const RouteArgs& p) {
       } else if (__ballot(close)) {
         // whole keys throughout
         if constexpr (BIASED) {
-          float s[V];
-#pragma unroll
-          for (int v = 0; v < V; ++v) s[v] = shifted_score(x[v], m, sigmoid);
+          float s[V], none[1];
+          shifted_scores<false>(x, m, sigmoid, s, none);
           biased_keys(s);
           all64();
         } else {
@@ -422,14 +464,21 @@ __device__ __forceinline__ void route_body(const RouteArgs& p) {
   }
 
   if (!balance) return;
-  // over waves, in their order
+  // over groups, in their order: threads that share an expert are a multiple of 64 apart
   routed_sum = group_sum<64>(routed_sum);
   if (lane == 0) routed_of[wave] = routed_sum;
   __syncthreads();
-  for (int e = threadIdx.x; e < p.E; e += kRouteThreads) {
-    float sum = 0.f;
+  constexpr int SHARE = kRouteThreads / (L * V), EACH = PER_BLOCK / SHARE;
+  const int e = threadIdx.x % (L * V), share = threadIdx.x / (L * V);
+  float sum = 0.f;
 #pragma unroll
-    for (int w = 0; w < kRouteWaves; ++w) sum += part[w][value_of<L>(e) * L + lane_of<L>(e)];
+  for (int i = 0; i < EACH; ++i) sum += part[share * EACH + i][e];
+  __syncthreads();
+  part[share][e] = sum;
+  __syncthreads();
+  if (share == 0 && e < p.E) {
+#pragma unroll
+    for (int i = 1; i < SHARE; ++i) sum += part[i][e];
     p.part_sums[size_t(blockIdx.x) * p.E + e] = sum;
     p.part_counts[size_t(blockIdx.x) * p.E + e] = count[e];
   }
@@ -471,6 +520,10 @@ __device__ __forceinline__ void route_finish_body(const RouteArgs& p) {
       count += c[i];
     }
   }
+  // (for the workgroup that ends last, on their way early)
+  int n = 0;
+  if (threadIdx.x < 64)
+    for (int b = threadIdx.x; b < p.nb; b += 64) n += p.part_routed[b];
   sums[part][col] = sum;
   counts[part][col] = count;
   __syncthreads();
@@ -491,8 +544,6 @@ __device__ __forceinline__ void route_finish_body(const RouteArgs& p) {
   __threadfence();
   double term = 0.0;
   for (int i = threadIdx.x; i < p.E; i += 64) term += __hip_atomic_load(&p.terms[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  int n = 0;
-  for (int b = threadIdx.x; b < p.nb; b += 64) n += p.part_routed[b];
   term = group_sum<64>(term);
   n = group_sum<64>(n);
   if (threadIdx.x == 0) {
@@ -511,7 +562,7 @@ struct RouteBwdArgs {
   const float* dloss;        // [1]
   void* dx;                  // [T][E]
   int T, E, k;
-  int sigmoid, renorm;
+  int sigmoid, renorm, counts_aligned;
   float scale;
 };
 
@@ -523,8 +574,7 @@ constexpr int kRouteBwdThreads = 256;
 //   softmax, plain   u_j = scale p_j dw_j, and - p_e sum_j u_j at every expert
 //   sigmoid, plain   u_j = scale s_j (1 - s_j) dw_j
 //   loss             f_e = dloss E / (k n^2) counts_e: p_e (f_e - sum p f) [(1 - s_e)]
-// A token without choices, and rows of the logits that it alone would read, add
-// nothing.  An expert that a token names twice gets both gradients, in their order.
+// A token without choices adds nothing, whatever its logits are.  An expert that a token names twice gets both gradients, in their order.
 // The u_j reach their experts' lanes through LDS.
 template <bool BF16, int L, int V>
 __device__ __forceinline__ void route_bwd_body(const RouteBwdArgs& p) {
@@ -537,41 +587,46 @@ __device__ __forceinline__ void route_bwd_body(const RouteBwdArgs& p) {
   const bool in = t < p.T;
   const size_t row = size_t(t) * p.E;
   const float inf = __builtin_inff();
+  const bool all = loss || !(p.renorm || sigmoid);
+  float x[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) x[v] = -inf;
+  if (all && in) load_row<BF16, L, V>(p.x, row, l, p.E, whole, -inf, x);
   int id = in && l < p.k ? p.ids[t * p.k + l] : -1;
   if (id >= p.E) id = -1;
   const uint64_t any = __ballot(id >= 0) >> base;
   const bool routed = (L == 64 ? any : any & 0xFFFFu) != 0;
-  float xs = -inf, dw = 0.f;
-  if (id >= 0) {
-    xs = logit<BF16>(p.x, row + id);
-    dw = p.scale * p.dw[t * p.k + l];
-  }
+  float xs = -inf;
+  const float dw = id >= 0 ? p.scale * p.dw[t * p.k + l] : 0.f;
+  // (a wave reads and writes its own tokens' rows only)
+  float* mine = at_expert[threadIdx.x / L];
 
   // what every expert gets: p_e (f_e - off), for sigmoid times 1 - s_e
   float pe[V], f[V], rest[V], off = 0.f, z = 1.f, m = 0.f;
-  const bool all = loss || !(p.renorm || sigmoid);
-  if (all) {
-    float x[V];
-    if (routed) {
-      load_row<BF16, L, V>(p.x, row, l, p.E, whole, -inf, x);
-    } else {
+  if (!all) {
+    if (id >= 0) xs = logit<BF16>(p.x, row + id);
+  } else {
+    // the choices' logits come through LDS, not by another read that waits for the ids
 #pragma unroll
-      for (int v = 0; v < V; ++v) x[v] = -inf;
-    }
-    uint32_t top = 0;
+    for (int i = 0; i < V / 4; ++i)
+      *reinterpret_cast<float4*>(mine + expert_of<L>(l, 4 * i)) = float4{x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]};
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    if (id >= 0) xs = mine[id];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
-    for (int v = 0; v < V; ++v) top = max(top, order_key(x[v]));
-    top = group_max<L>(top);
-    m = top ? key_value(top) : 0.f;
+    for (int v = 0; v < V; ++v) x[v] = routed ? x[v] : -inf;
+    m = x[0];
+#pragma unroll
+    for (int v = 1; v < V; ++v) m = __builtin_elementwise_maximum(m, x[v]);
+    m = group_reduce<L>(m, [](float a, float b) { return __builtin_elementwise_maximum(a, b); });
+    const bool open = m != -inf;
+    if (!open) m = 0.f;
+    shifted_scores<true>(x, m, sigmoid, pe, rest);
     z = 0.f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      pe[v] = shifted_score(x[v], m, sigmoid);
-      rest[v] = sigmoid ? one_minus_sigmoid(x[v]) : 1.f;
-      z += pe[v];
-    }
+    for (int v = 0; v < V; ++v) z += pe[v];
     z = group_sum<L>(z);
-    if (top == 0) z = 1.f;                  // no expert of the row is open
+    if (!open) z = 1.f;
     const float r = 1.f / z;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -581,9 +636,10 @@ __device__ __forceinline__ void route_bwd_body(const RouteBwdArgs& p) {
     if (loss) {
       const double n = *p.routed;
       const float c = n > 0.0 ? float(double(*p.dloss) * p.E / (double(p.k) * n * n)) : 0.f;
+      load_row<false, L, V>(p.counts, 0, l, p.E, whole && p.counts_aligned, 0.f, f);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        f[v] = c * float(p.counts[min(expert_of<L>(l, v), p.E - 1)]);
+        f[v] = c * float(__float_as_int(f[v]));
         off = __builtin_fmaf(pe[v], f[v], off);
       }
       off = group_sum<L>(off);
@@ -610,8 +666,6 @@ __device__ __forceinline__ void route_bwd_body(const RouteBwdArgs& p) {
   }
   if (!p.renorm && !sigmoid) off += group_sum<L>(u);
 
-  // (a wave reads and writes its own tokens' rows only)
-  float* mine = at_expert[threadIdx.x / L];
 #pragma unroll
   for (int i = 0; i < V / 4; ++i) *reinterpret_cast<float4*>(mine + expert_of<L>(l, 4 * i)) = float4{0.f, 0.f, 0.f, 0.f};
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");

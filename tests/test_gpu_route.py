@@ -143,6 +143,23 @@ def test_route_bias_that_tells_near_sums_apart():
     check(x, k, "sigmoid", True, bias=bias)
 
 
+@pytest.mark.parametrize("E,k", [(64, 4), (256, 8), (1024, 8), (64, 20)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_route_lowest_values_are_open(E, k, dtype):
+    """The type's lowest value masks softly: chosen where nothing else is left, also as
+    the last expert; only -inf closes."""
+    x = torch.full((6, E), torch.finfo(dtype).min)
+    x[1] = -INF
+    x[1, E - 1] = torch.finfo(dtype).min
+    x[2, : E - 2] = -INF
+    x[3, 5] = 1.0
+    x[4, E - 1] = torch.finfo(dtype).max
+    x[5, ::2] = -torch.finfo(dtype).tiny
+    r, ids = check(x.to(dtype), k, "softmax", True)
+    assert ids[0].tolist() == list(range(k)) and ids[1, :2].tolist() == [E - 1, -1]
+    check(x.to(dtype), k, "sigmoid", False, bias=torch.zeros(E))
+
+
 @pytest.mark.parametrize("mask_type", [torch.bool, torch.uint8])
 def test_route_mask(mask_type):
     x = logits(203, 60, torch.float32, 7, "closed")
