@@ -1,6 +1,7 @@
-"""A mixture-of-experts feed-forward layer in FP8: training steps and a decode step.
+"""A mixture-of-experts feed-forward layer in FP8: training steps and a decode step,
+of the layer alone or of a stack of blocks around it.
 
-    python examples/moe_layer.py [--tokens 2048] [--steps 20]
+    python examples/moe_layer.py [--tokens 2048] [--steps 20] [--blocks 2]
 
 Every expert computes y = (u g / (1 + exp(-g))) W2^T with [g | u] = x W13^T.  The
 layer keeps nothing between its passes but 8-bit operands: the quantised tokens,
@@ -9,6 +10,10 @@ the gated activation's checkpoint and its result.
   forward   sort -> permute + quantise -> product -> gated activation -> product -> combine
   backward  combine's gradient -> product -> gated activation's gradient -> product -> combine,
             and a weight gradient for each product
+
+A block normalises the residual stream, routes its tokens (with a balance loss), runs the
+layer and adds its output, normalised and gated, to the stream; what stands between two
+blocks is one call.  A training step of the stack clips its gradients.
 """
 import argparse
 import os
@@ -85,10 +90,117 @@ class MoELayer:
         return dg.moe_combine(y, plan.slot_row, weights)
 
 
+class Block(NamedTuple):
+    """A layer and what is around it in a block; float32 parameters."""
+    layer: MoELayer
+    w_pre: torch.Tensor       # [hidden] of the norm before it
+    router: torch.Tensor      # [hidden][experts]
+    w_post: torch.Tensor      # [hidden] of the norm after it
+    gate: torch.Tensor        # [hidden]
+
+    @property
+    def parameters(self):
+        return [self.w_pre, self.router, self.w_post, self.gate, self.layer.w13, self.layer.w2]
+
+
+class MoEStack:
+    """Blocks one after another on a bfloat16 residual stream, and a last norm."""
+
+    def __init__(self, blocks, experts, top_k, hidden, inner, device="cuda", generator=None, balance=0.01):
+        ones = lambda: torch.ones(hidden, device=device)
+        self.top_k, self.alpha, self.balance = top_k, blocks ** -0.5, balance
+        self.blocks = [Block(MoELayer(experts, hidden, inner, device, generator), ones(),
+                             torch.randn(hidden, experts, device=device, generator=generator) * hidden ** -0.5,
+                             ones(), ones()) for _ in range(blocks)]
+        self.w_last = ones()
+
+    @property
+    def parameters(self):
+        return [p for b in self.blocks for p in b.parameters] + [self.w_last]
+
+    def _norms(self):
+        return [b.w_pre for b in self.blocks] + [self.w_last]
+
+    def forward(self, x, mask=None):
+        """(out [T][hidden], the blocks' balance losses, what backward needs) of the
+        stream x (bfloat16); mask [T]: False for rows that hold no token."""
+        norms, saved, losses = self._norms(), [], []
+        stream, n = x, dg.residual_norm(x, w_pre=norms[0]).N
+        for b, w_next in zip(self.blocks, norms[1:]):
+            logits = n.float() @ b.router
+            r = dg.moe_route(logits, self.top_k, mask=mask)
+            y, of_layer = b.layer.forward(n, r.ids, r.weights)
+            after = dg.residual_norm(stream, y, w_post=b.w_post, gate=b.gate, alpha=self.alpha, w_pre=w_next)
+            saved.append((n, logits, r, y, of_layer, after.R))
+            losses.append(r.loss)
+            stream, n = after.R, after.N
+        return n, losses, (x, saved)
+
+    def backward(self, dout, state):
+        """Gradients (dx, those of `parameters`) of dout (bfloat16) and of `balance`
+        times the balance losses."""
+        x, saved = state
+        norms, grads, dstream, dn = self._norms(), [None] * len(self.blocks), None, dout
+        dloss = torch.full((), self.balance, device=x.device)
+        dw_pre = [None] * len(norms)
+        for i in reversed(range(len(self.blocks))):
+            b, (n, logits, r, y, of_layer, after) = self.blocks[i], saved[i]
+            g = dg.residual_norm_bwd(dstream, dn, after, y, w_post=b.w_post, gate=b.gate, alpha=self.alpha,
+                                     w_pre=norms[i + 1])
+            dw_pre[i + 1] = g.dw_pre
+            dtokens, dweights, dw13, dw2 = b.layer.backward(g.dY, of_layer)
+            dlogits = dg.moe_route_bwd(dweights, logits, r.ids, dloss=dloss, counts=r.counts, routed=r.routed)
+            dn = (dtokens.float() + dlogits @ b.router.t()).bfloat16()
+            grads[i] = [None, n.float().t() @ dlogits, g.dw_post, g.dgate, dw13, dw2]
+            dstream = g.dR
+        first = dg.residual_norm_bwd(dstream, dn, x, w_pre=norms[0])
+        dw_pre[0] = first.dw_pre
+        for d, of_block in zip(dw_pre, grads):
+            of_block[0] = d
+        return first.dR, [d for of_block in grads for d in of_block] + [dw_pre[-1]]
+
+    def update(self, grads, lr, max_norm):
+        """A step along the gradients, clipped in place; their norm before."""
+        norm = dg.grad_norm(grads)
+        dg.clip_grads(grads, norm, max_norm)
+        for p, d in zip(self.parameters, grads):
+            p -= lr * d
+        for b in self.blocks:
+            b.layer.refresh()
+        return norm
+
+    def decode(self, x):
+        """The forward pass for a few tokens: no load, packed segments, no checkpoint."""
+        norms = self._norms()
+        stream, n = x, dg.residual_norm(x, w_pre=norms[0]).N
+        for b, w_next in zip(self.blocks, norms[1:]):
+            r = dg.moe_route(n.float() @ b.router, self.top_k, balance=False)
+            y = b.layer.decode(n, r.ids, r.weights)
+            stream, n, _, _ = dg.residual_norm(stream, y, w_post=b.w_post, gate=b.gate, alpha=self.alpha, w_pre=w_next)
+        return n
+
+
 def route(x, router, k):
     """Expert ids and router weights: the k largest logits, softmax over them."""
     top = torch.topk(x.float() @ router, k, dim=1)
     return top.indices, torch.softmax(top.values, dim=1)
+
+
+def train_stack(args, generator):
+    make = lambda: MoEStack(args.blocks, args.experts, args.top_k, args.hidden, args.inner, generator=generator)
+    stack, teacher = make(), make()
+    x = torch.randn(args.tokens, args.hidden, device="cuda", generator=generator).bfloat16()
+    target = teacher.forward(x)[0].float()
+    for step in range(args.steps):
+        out, losses, saved = stack.forward(x)
+        diff = out.float() - target
+        _, grads = stack.backward((diff / args.tokens).bfloat16(), saved)
+        norm = stack.update(grads, args.lr, 1.0)
+        print(f"step {step}: loss {0.5 * float(diff.square().sum()) / args.tokens:.4f}, balance "
+              f"{float(sum(losses)) / args.blocks:.3f}, gradient norm {float(norm):.3f}", flush=True)
+    few = min(4, args.tokens)
+    one, whole = stack.decode(x[:few].contiguous()).float(), stack.forward(x)[0][:few].float()
+    print(f"decode of {few} tokens: relative difference from the whole batch {float((one - whole).norm() / whole.norm()):.2e}")
 
 
 def main():
@@ -100,8 +212,12 @@ def main():
     ap.add_argument("--tokens", type=int, default=2048)
     ap.add_argument("--steps", type=int, default=20)
     ap.add_argument("--lr", type=float, default=0.05)
+    ap.add_argument("--blocks", type=int, default=0, help="blocks of a stack; 0: the layer alone")
     args = ap.parse_args()
     g = torch.Generator(device="cuda").manual_seed(0)
+    if args.blocks > 0:
+        train_stack(args, g)
+        return
     layer = MoELayer(args.experts, args.hidden, args.inner, generator=g)
     teacher = MoELayer(args.experts, args.hidden, args.inner, generator=g)
     router = torch.randn(args.hidden, args.experts, device="cuda", generator=g) * args.hidden ** -0.5
