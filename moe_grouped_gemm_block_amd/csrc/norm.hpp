@@ -324,19 +324,20 @@ __device__ __forceinline__ void norm_body(const NormArgs& p) {
   }
   Eight<RB> r, r_next;
   Eight<YB> y, y_next;
-  auto load = [&](int t, int c, Eight<RB>& r, Eight<YB>& y) {
+  auto load = [&](uint32_t t, int c, Eight<RB>& r, Eight<YB>& y) {
     r = load_eight<RB, WHOLE, !WIDE>(p.R, size_t(t) * p.H, c, p.H);
     if (block) y = load_eight<YB, WHOLE, !WIDE>(p.Y, size_t(t) * p.H, c, p.H);
   };
   if (!WIDE) load(blockIdx.x, c0, r_next, y_next);
-  for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
+  // (unsigned: the rows after the last may lie past 2^31)
+  for (uint32_t t = blockIdx.x; t < uint32_t(p.T); t += gridDim.x) {
     const size_t row = size_t(t) * p.H;
     const F token = p.gate_kind == kGateToken ? p.gate[t] : 1.f;
     if (!WIDE) {
       // the next row is on its way while this one is computed
       r = r_next;
       y = y_next;
-      if (t + int(gridDim.x) < p.T) load(t + gridDim.x, c0, r_next, y_next);
+      if (t + gridDim.x < uint32_t(p.T)) load(t + gridDim.x, c0, r_next, y_next);
     }
     // squares over the row: of Y, then of R'
     auto mean_rstd = [&](auto narrow, auto wide) -> F {

@@ -188,6 +188,36 @@ def test_norm_many_rows():
     check(problem(700, 4096, B, B))
 
 
+def test_norm_past_2_31_elements():
+    """Rows far behind give what they give alone, forward and backward."""
+    T, H = 1_050_000, 2056
+    g = torch.Generator(device=DEV).manual_seed(1)
+    R = torch.empty(T, H, dtype=B, device=DEV)
+    Y = torch.empty(T, H, dtype=B, device=DEV)
+    for at in range(0, T, 150_000):
+        R[at:at + 150_000].normal_(generator=g)
+        Y[at:at + 150_000].normal_(generator=g)
+    w, gate = torch.rand(H, device=DEV, generator=g) + 0.5, torch.rand(T, 1, device=DEV, generator=g)
+    rows = [0, 777_777, T - 2, T - 1]
+    few = [t[rows].contiguous() for t in (R, Y, gate)]
+    out = dg.residual_norm(R, Y, w_post=w, gate=gate, w_pre=w)
+    alone = dg.residual_norm(few[0], few[1], w_post=w, gate=few[2], w_pre=w)
+    assert torch.equal(out.R[rows], alone.R) and torch.equal(out.N[rows], alone.N)
+    got = dg.residual_norm_bwd(R, Y, out.R, Y, w_post=w, gate=gate, w_pre=w)
+    del out
+    one = dg.residual_norm_bwd(few[0], few[1], alone.R, few[1], w_post=w, gate=few[2], w_pre=w)
+    assert torch.equal(got.dR[rows], one.dR) and torch.equal(got.dY[rows], one.dY) and torch.equal(got.dgate[rows], one.dgate)
+
+
+def test_norm_rows_of_one_column_to_the_last():
+    """As many rows as there are workgroups several thousand times over."""
+    T = 30_000_000
+    x = torch.ones(T, 1, device=DEV)
+    x[-1] = -3
+    out = dg.residual_norm(x, w_pre=torch.full((1,), 2.0, device=DEV), dtype="f32")
+    assert bool(((out.N[:-1] - 2).abs() < 1e-5).all()) and abs(float(out.N[-1]) + 2) < 1e-5
+
+
 # ---------------------------------------------------------------- backward
 
 def check_bwd(p, alpha=1.0, eps=1e-6, seed=3, with_dR=True, stream=None):

@@ -215,6 +215,20 @@ def test_route_many_tokens_one_expert():
     assert n(r.counts)[[5, 20]].tolist() == [T, T]
 
 
+def test_route_more_tokens_than_a_grid_takes_at_once():
+    """Millions of tokens: every workgroup in several turns also without the load."""
+    T, E = 4_400_000, 4
+    x = torch.randn(T, E, device=DEV, generator=torch.Generator(device=DEV).manual_seed(3))
+    want = x.argmax(1).int()
+    a = dg.moe_route(x, 1, balance=False)
+    b = dg.moe_route(x, 1)
+    assert torch.equal(a.ids[:, 0], want) and torch.equal(b.ids[:, 0], want) and int(b.routed) == T
+    assert torch.equal(b.counts.long(), torch.bincount(want, minlength=E)) and bool((a.weights == 1).all())
+    dx = dg.moe_route_bwd(torch.ones(T, 1, device=DEV), x, a.ids, renormalise=False)
+    last = dg.moe_route_bwd(torch.ones(5, 1, device=DEV), x[-5:].contiguous(), a.ids[-5:].contiguous(), renormalise=False)
+    assert torch.equal(dx[-5:], last)
+
+
 def test_route_repeatable_and_on_a_side_stream():
     x = logits(5000, 200, torch.float32, 10)
     a, _ = check(x, 8, "sigmoid", True)
