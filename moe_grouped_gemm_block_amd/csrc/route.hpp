@@ -323,32 +323,42 @@ __device__ __forceinline__ void route_body(const RouteArgs& p) {
     for (int v = 0; v < V; ++v)
       key[v] = ((key[v] + kClosedKeys) & ~NUMBER) | (NUMBER - uint32_t(expert_of<L>(l, v)));
     uint32_t mine = 0, last = 0;
-    [[maybe_unused]] bool close = false, more = false;
     bool left = true;                               // experts to choose from
-    int n = p.k;                                    // choices that there are
-    for (int j = 0; WHOLE_KEYS ? j < p.k : j <= L; ++j) {
+    auto choose = [&] {
       uint32_t best = 0;
 #pragma unroll
       for (int v = 0; v < V; ++v) best = max(best, key[v] - last);
-      uint32_t g = group_max<L>(best) + last;
-      left = left && g > kClosedKeys;
-      if (!left) g = 0;
-      if constexpr (!WHOLE_KEYS) {
-        more = false;
-        if (j > 0 && left) {
-          const uint32_t high = (g | NUMBER) - kClosedKeys, low = (last & ~NUMBER) - kClosedKeys;   // bounds of their keys
-          if constexpr (BIASED) more = !(key_value(low) - key_value(high) > biased_tolerance(key_value(low), most, sigmoid));
-          else more = high >= low;
-        }
-        if (j >= p.k && !__ballot(more)) {
-          n = j;
-          break;
-        }
-        close = close || more;
-        n = j;
+      last += group_max<L>(best);
+      left = left && last > kClosedKeys;
+      if (!left) last = 0;
+    };
+    for (int j = 0; j < p.k; ++j) {
+      choose();
+      if (l == j) mine = last;
+    }
+    [[maybe_unused]] bool close = false, more = false;
+    int n = p.k;                                    // choices that there are
+    if constexpr (!WHOLE_KEYS) {
+      // whether the second key, in order behind the first, may be of as large a value
+      auto too_close = [&](uint32_t first, uint32_t second) {
+        const uint32_t high = (second | NUMBER) - kClosedKeys, low = (first & ~NUMBER) - kClosedKeys;
+        if constexpr (BIASED) return !(key_value(low) - key_value(high) > biased_tolerance(key_value(low), most, sigmoid));
+        else return high >= low;
+      };
+      choose();                                     // the one behind the last
+      uint32_t behind = L == 16 ? row_rotated<15>(mine) : __shfl(mine, (lane + 1) & 63, 64);
+      if (l == p.k - 1) behind = last;
+      const uint64_t pairs = (__ballot(l < p.k && behind != 0 && too_close(mine, behind)) >> base) &
+                             (L == 64 ? ~uint64_t(0) : uint64_t(0xFFFF));
+      close = pairs != 0;
+      more = (pairs >> (p.k - 1)) & 1;
+      while (__ballot(more) && n < L) {
+        if (l == n) mine = last;
+        ++n;
+        const uint32_t before = last;
+        choose();
+        more = last != 0 && too_close(before, last);
       }
-      if (l == j) mine = g;
-      last = g;
     }
     int id = mine ? int(NUMBER - (mine & NUMBER)) : -1;
 
