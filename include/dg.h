@@ -503,8 +503,8 @@ typedef enum {
  *   routed      : int32 [1], their number n
  *   loss        : float32 [1], E / (top_k n^2) sum_e counts_e prob_sums_e (the
  *                 balance loss: 1 where both are even), 0 if n = 0
- *   workspace   : dg_moe_route_workspace() bytes, 8-byte aligned, in use until the work
- *                 is done
+ *   workspace   : dg_moe_route_workspace() bytes (null if that is 0), 8-byte aligned, in
+ *                 use until the work is done
  *
  * counts, prob_sums, routed and loss are all null where no load is wanted (decode);
  * workspace is then not used.  Shares whose scores all underflow are those of the

@@ -455,7 +455,7 @@ PyObject* moe_route(PyObject*, PyObject* const* a, Py_ssize_t n) {
     sums = part(floats, 0, {E});
     loss = part(floats, E, {});
     weights = part(floats, E + 1, {T, k});
-    work = create({ws}, at::kByte, x);
+    if (ws) work = create({ws}, at::kByte, x);
   } else {
     ids = create({T, k}, at::kInt, x);
     weights = create({T, k}, at::kFloat, x);
@@ -463,7 +463,7 @@ PyObject* moe_route(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int st = lib.moe_route(x.data_ptr(), code, bias, mask, T, E, k, score, renormalise, scale, data<int32_t>(ids),
                                data<float>(weights), balance ? data<int32_t>(counts) : nullptr,
                                balance ? data<float>(sums) : nullptr, balance ? data<int32_t>(routed) : nullptr,
-                               balance ? data<float>(loss) : nullptr, balance ? work.data_ptr() : nullptr, stream());
+                               balance ? data<float>(loss) : nullptr, ws && balance ? work.data_ptr() : nullptr, stream());
   if (st != DG_OK) return failure(st, "dg_moe_route");
   return tuple(ids, weights, counts, sums, routed, loss);
   END_HANDLE_TH_ERRORS

@@ -36,6 +36,7 @@ namespace dg {
 DG_ROUTE_KERNELS(bf16, true)
 DG_ROUTE_KERNELS(f32, false)
 DG_BLOCK_KERNEL(dg_moe_route_finish, kFinishExperts * kFinishParts, RouteArgs, route_finish_body)
+DG_BLOCK_KERNEL(dg_moe_route_finish_one, kFinishExperts * kFinishParts, RouteArgs, route_finish_one_body)
 #undef DG_ROUTE_KERNELS
 
 // (templates: stream and value types, codes, whole rows, wide rows)
@@ -67,15 +68,27 @@ int check_route(int64_t T, int64_t E, int top_k) {
 }
 
 // Lanes and logits per lane: a row of 16 lanes holds up to 256 experts and 16 choices.
-int route_lanes(int64_t E, int top_k) { return E <= 256 && top_k <= 16 ? 16 : 64; }
-int route_variant(int64_t E, int top_k) {
-  if (route_lanes(E, top_k) == 16) return E <= 64 ? 0 : 1;
+// More than 64 experts of few tokens go over a whole wave each, which ends sooner, many
+// over a row, which takes fewer instructions a token (256 experts, 8 choices, biased
+// sigmoid with the load, row / wave: 256 tokens 17.9 / 12.9 us, 4096 18.4 / 15.4, 8192 18.7
+// / 19.7, 16384 20.3 / 28.9; gradient 4096 5.4 / 4.9, 8192 7.4 / 8.0).
+int route_lanes(int64_t T, int64_t E, int top_k) {
+  return E <= 256 && top_k <= 16 && (E <= 64 || T > 4096) ? 16 : 64;
+}
+int route_variant(int64_t T, int64_t E, int top_k) {
+  if (route_lanes(T, E, top_k) == 16) return E <= 64 ? 0 : 1;
   return E <= 256 ? 2 : 3;
 }
 
+// Workgroups.  With the load a single one takes few tokens, which saves the second launch
+// (64 experts, a row of lanes a token: 128 tokens in two turns 6.9 us, by two launches 9.3;
+// a wave a token, 256 experts: 16 tokens in one turn 6.2 us, 64 in four 16.5, by two
+// launches 9.6).
 int64_t route_blocks(int64_t T, int64_t E, int top_k, bool balance) {
-  const int64_t per = dg::kRouteThreads / route_lanes(E, top_k);
-  return std::min<int64_t>(std::max<int64_t>(1, ceil_div(T, per)), balance ? dg::kRouteMaxBlocks : 65536);
+  const int lanes = route_lanes(T, E, top_k);
+  if (balance && T <= (lanes == 16 ? 128 : 16)) return 1;
+  return std::min<int64_t>(std::max<int64_t>(1, ceil_div(T, dg::kRouteThreads / lanes)),
+                           balance ? dg::kRouteMaxBlocks : 65536);
 }
 
 bool valid_scores(int score, int renormalise, float scale) {
@@ -243,7 +256,8 @@ extern "C" {
 int64_t dg_moe_route_workspace(int64_t T, int64_t E, int top_k) {
   const int st = check_route(T, E, top_k);
   if (st != DG_OK) return st;
-  return route_blocks(T, E, top_k, true) * (8 * E + 4) + 8 * E + 4;
+  const int64_t nb = route_blocks(T, E, top_k, true);
+  return nb > 1 ? nb * (8 * E + 4) + 8 * E + 4 : 0;
 }
 
 int dg_moe_route(const void* logits, int dtype, const float* bias, const uint8_t* mask, int64_t T, int64_t E, int top_k,
@@ -257,15 +271,15 @@ int dg_moe_route(const void* logits, int dtype, const float* bias, const uint8_t
     return DG_ERR_INVALID_ARG;
   if (!aligned(counts, 4) || !aligned(prob_sums, 4) || !aligned(routed, 4) || !aligned(loss, 4) || !aligned(bias, 4))
     return DG_ERR_INVALID_ARG;
-  if (balance && bad(workspace, 8)) return DG_ERR_INVALID_ARG;
+  const int64_t nb = route_blocks(T, E, top_k, balance);
+  if (balance && nb > 1 && bad(workspace, 8)) return DG_ERR_INVALID_ARG;
   if (T > 0 && (bad(logits, 16) || bad(ids, 4) || bad(weights, 4))) return DG_ERR_INVALID_ARG;
   if (T == 0 && !balance) return DG_OK;
-  const int64_t nb = route_blocks(T, E, top_k, balance);
-  double* terms = static_cast<double*>(workspace);
-  float* part = reinterpret_cast<float*>(terms + E);
-  int32_t* ints = reinterpret_cast<int32_t*>(part + nb * E);
-  dg::RouteArgs a{logits, bias, mask, ids, weights, counts, prob_sums, routed, loss, part, ints, ints + nb * E, terms,
-                  ints + nb * E + nb, int(T), int(E), top_k, int(nb), score == DG_SCORE_SIGMOID, renormalise,
+  double* terms = static_cast<double*>(nb > 1 && balance ? workspace : nullptr);
+  float* part = terms ? reinterpret_cast<float*>(terms + E) : nullptr;
+  int32_t* ints = terms ? reinterpret_cast<int32_t*>(part + nb * E) : nullptr;
+  dg::RouteArgs a{logits, bias, mask, ids, weights, counts, prob_sums, routed, loss, part, ints, terms ? ints + nb * E : nullptr, terms,
+                  terms ? ints + nb * E + nb : nullptr, int(T), int(E), top_k, int(nb), score == DG_SCORE_SIGMOID, renormalise,
                   aligned(bias, 16), scale};
 #define DG_ROUTE_TABLE(T)                                                                                       \
   {{dg::dg_moe_route_##T##_16x4, dg::dg_moe_route_##T##_16x16, dg::dg_moe_route_##T##_64x4,                     \
@@ -274,9 +288,11 @@ int dg_moe_route(const void* logits, int dtype, const float* bias, const uint8_t
     dg::dg_moe_route_##T##_64x16_bias}}
   static void (*const kernels[2][2][4])(dg::RouteArgs) = {DG_ROUTE_TABLE(f32), DG_ROUTE_TABLE(bf16)};
 #undef DG_ROUTE_TABLE
-  const int st1 = launch(kernels[dtype == DG_IN_BF16][bias != nullptr][route_variant(E, top_k)], a, nb,
+  const int st1 = launch(kernels[dtype == DG_IN_BF16][bias != nullptr][route_variant(T, E, top_k)], a, nb,
                          dg::kRouteThreads, stream);
-  if (st1 != DG_OK || !balance) return st1;
+  if (st1 != DG_OK || !balance || nb == 1) return st1;
+  if (nb * E <= dg::kFinishOne)
+    return launch(dg::dg_moe_route_finish_one, a, 1, dg::kFinishExperts * dg::kFinishParts, stream);
   return launch(dg::dg_moe_route_finish, a, ceil_div(E, dg::kFinishExperts), dg::kFinishExperts * dg::kFinishParts, stream);
 }
 
@@ -297,8 +313,8 @@ int dg_moe_route_bwd(const float* dweights, const void* logits, int dtype, const
    dg::dg_moe_route_bwd_##T##_64x16}
   static void (*const kernels[2][4])(dg::RouteBwdArgs) = {DG_ROUTE_TABLE(f32), DG_ROUTE_TABLE(bf16)};
 #undef DG_ROUTE_TABLE
-  return launch(kernels[dtype == DG_IN_BF16][route_variant(E, top_k)], a,
-                ceil_div(T, dg::kRouteBwdThreads / route_lanes(E, top_k)), dg::kRouteBwdThreads, stream);
+  return launch(kernels[dtype == DG_IN_BF16][route_variant(T, E, top_k)], a,
+                ceil_div(T, dg::kRouteBwdThreads / route_lanes(T, E, top_k)), dg::kRouteBwdThreads, stream);
 }
 
 int dg_residual_norm(const void* R, int r_dtype, const void* Y, int dtype, const float* w_post, const float* gate,

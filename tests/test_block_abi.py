@@ -34,7 +34,7 @@ SHARED = [(dict(dt=2), INVALID), (dict(T=-1), INVALID), (dict(T=BIG), INVALID), 
 
 @pytest.mark.parametrize("kw,want", SHARED + [
     (dict(w=None), INVALID), (dict(bias=P + 2), INVALID), (dict(sums=None), INVALID), (dict(loss=None), INVALID),
-    (dict(loss=P + 2), INVALID), (dict(ws=None), INVALID), (dict(ws=P + 4), INVALID)])
+    (dict(loss=P + 2), INVALID), (dict(T=1000, ws=None), INVALID), (dict(T=1000, ws=P + 4), INVALID)])
 def test_route_validation(kw, want):
     assert call(dg.dg_moe_route, ROUTE, kw) == want
 
@@ -49,7 +49,8 @@ def test_route_empty_work_and_workspace():
     none = dict(counts=None, sums=None, routed=None, loss=None, ws=None)
     assert call(dg.dg_moe_route, ROUTE, dict(none, T=0, x=None, ids=None, w=None)) == OK
     assert call(dg.dg_moe_route_bwd, ROUTE_BWD, dict(T=0, x=None, ids=None, dw=None, dx=None)) == OK
-    assert dg.dg_moe_route_workspace(0, 64, 2) > 0 and dg.dg_moe_route_workspace(1 << 29, 1024, 2) > 0
+    assert dg.dg_moe_route_workspace(0, 64, 2) == dg.dg_moe_route_workspace(20, 64, 2) == 0
+    assert dg.dg_moe_route_workspace(1000, 64, 2) > 0 and dg.dg_moe_route_workspace(1 << 29, 1024, 2) > 0
     for T, E, k, want in [(-1, 4, 1, INVALID), (5, 0, 1, INVALID), (5, 4, 5, INVALID), (5, 1025, 1, UNSUP),
                           (5, 100, 65, UNSUP)]:
         assert dg.dg_moe_route_workspace(T, E, k) == want
