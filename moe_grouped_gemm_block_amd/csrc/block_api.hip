@@ -119,6 +119,8 @@ int64_t norm_bwd_blocks(int64_t T, int64_t H) {
   return std::min(ceil_div(T, norm_bwd_groups(H)), std::min<int64_t>(most, 512));
 }
 
+constexpr int64_t kNormAloneTurns = 2;
+
 int check_norm(int r_dtype, int dtype, const void* Y, const float* w_post, const float* gate, int gate_kind,
                float alpha, const float* w_pre, float eps, int64_t T, int64_t H) {
   if (!valid_type(r_dtype) || !valid_type(dtype)) return DG_ERR_INVALID_ARG;
@@ -362,17 +364,22 @@ int dg_residual_norm_bwd(const void* dR, const void* dN, const void* R, int r_dt
   if ((w_pre && bad(dw_pre, 4)) || (w_post && bad(dw_post, 4)) || (channel && bad(dgate, 4))) return DG_ERR_INVALID_ARG;
   if ((!w_pre && dw_pre) || (!w_post && dw_post) || (gate_kind == DG_GATE_NONE && dgate)) return DG_ERR_INVALID_ARG;
   const bool pre = w_pre != nullptr, post = w_post != nullptr || channel;
-  const int64_t nb = norm_bwd_blocks(T, H);
+  // few rows: one workgroup, whose sums are the gradients themselves (unless two gradients
+  // come of one sum), and no second launch (4 rows of 2048 8.2 us, by two launches 9.4; 2 of
+  // 4096 7.0 and 9.3)
+  const bool alone = T > 0 && T <= kNormAloneTurns * norm_bwd_groups(H) && !(w_post && channel) &&
+                     aligned(dw_pre, 16) && aligned(dw_post, 16) && (!channel || aligned(dgate, 16));
+  const int64_t nb = alone ? 1 : norm_bwd_blocks(T, H);
   float* part = static_cast<float*>(workspace);
-  float* part_pre = pre ? part : nullptr;
-  float* part_post = post ? part + (pre ? nb * H : 0) : nullptr;
+  float* part_pre = !pre ? nullptr : alone ? dw_pre : part;
+  float* part_post = !post ? nullptr : alone ? (w_post ? dw_post : dgate) : part + (pre ? nb * H : 0);
   if (T > 0) {
     if (bad(dR_out, 16) || !aligned(dR, 16) || (token && bad(dgate, 4))) return DG_ERR_INVALID_ARG;
     if (pre ? bad(R, 16) || bad(dN, 16) : dN != nullptr || dR == nullptr) return DG_ERR_INVALID_ARG;
     if ((dY != nullptr) != (Y != nullptr) || !aligned(dY, 16)) return DG_ERR_INVALID_ARG;
     if (dR_out == dR || dR_out == R || dR_out == dN || dR_out == Y || dR_out == dY) return DG_ERR_INVALID_ARG;
     if (dY && (dY == Y || dY == R || dY == dR || dY == dN)) return DG_ERR_INVALID_ARG;
-    if ((pre || post) && bad(workspace, 16)) return DG_ERR_INVALID_ARG;
+    if ((pre || post) && !alone && bad(workspace, 16)) return DG_ERR_INVALID_ARG;
     const bool rb = r_dtype == DG_IN_BF16, yb = dtype == DG_IN_BF16, whole = H % 8 == 0;
     const int64_t most = norm_bwd_most(H, rb && yb);
     const bool wide = norm_wide(H, most);
@@ -385,7 +392,7 @@ int dg_residual_norm_bwd(const void* dR, const void* dN, const void* R, int r_dt
     const int st1 = launch(kernel, a, nb, threads * norm_bwd_groups(H), stream);
     if (st1 != DG_OK) return st1;
   }
-  if (!pre && !post) return DG_OK;
+  if ((!pre && !post) || alone) return DG_OK;
   // (without rows the sums are zeros)
   const int blocks = int(ceil_div(H, 32));
   dg::NormColumnsArgs c{part_pre, part_post, w_post, channel ? gate : nullptr, dw_pre, dw_post, channel ? dgate : nullptr,
