@@ -81,16 +81,20 @@ def log(*a):
 
 
 def kernel_source_hash() -> str:
-    """Hash of the products' and the quantiser's kernel sources and of the build script (its
-    compiler flags shape the code); the operators around the products are not measured here."""
+    """Hash of the products' and the quantiser's kernel sources and of their compiler flags;
+    the operators around the products and around a block are not measured here."""
+    from moe_grouped_gemm_block_amd import build
+
     h = hashlib.sha256()
-    around = {"binding.cpp", "kernels_wgrad.hip", "moe.hpp", "moe_api.hip", "swiglu.hpp", "wgrad.hpp"}
+    around = {"binding.cpp", "kernels_wgrad.hip", "moe.hpp", "moe_api.hip", "swiglu.hpp", "wgrad.hpp",
+              "block_api.hip", "clip.hpp", "groups.hpp", "host.hpp", "norm.hpp", "route.hpp"}
     files = sorted(f for f in glob.glob(os.path.join(ROOT, "moe_grouped_gemm_block_amd", "csrc", "*"))
                    if os.path.basename(f) not in around)
-    files.append(os.path.join(ROOT, "moe_grouped_gemm_block_amd", "build.py"))
     for f in files:
         h.update(os.path.basename(f).encode())
         h.update(open(f, "rb").read())
+    # (the flags that are not paths)
+    h.update("\0".join(f for f in build.compile_command("", "") if not os.path.isabs(f)).encode())
     return h.hexdigest()[:16]
 
 
