@@ -6,7 +6,9 @@
  * A scales, dg_grouped_gemm_fp8_segments serves decode-time MoE.  The dg_moe_*,
  * dg_swiglu_* and dg_grouped_wgrad_fp8 calls are what a mixture-of-experts layer
  * needs around its products: tokens sorted by expert and back, the gated
- * activation with an 8-bit checkpoint, and the backward passes.
+ * activation with an 8-bit checkpoint, and the backward passes.  dg_moe_route,
+ * dg_residual_norm, dg_grad_norm, dg_clip_grads and the gradients of the first two
+ * make that layer a block of a model.
  *
  * The operation (DeepGEMM FP8-for-MoE page, 2kiu.com/news/5461879,
  * section 2.1 "block-wise scaling"; FP32 accumulation, section 3.3):
@@ -597,7 +599,7 @@ int dg_grad_norm(const void* const* grads, const int64_t* sizes, const int* dtyp
 /*
  * Clipping: outs[i] = grads[i] min(1, max_norm / norm), with norm float32 [1] on the
  * device.  outs[i] may be grads[i] (of the same type then) and must not overlap
- * anything else in the lists (DG_ERR_INVALID_ARG).  A norm of NaN gives NaN, an
+ * anything else in the lists, nor norm (DG_ERR_INVALID_ARG).  A norm of NaN gives NaN, an
  * infinite one zeros and, for infinite elements, NaN.  max_norm finite and positive.
  */
 int dg_clip_grads(const void* const* grads, const int64_t* sizes, const int* dtypes, int count,

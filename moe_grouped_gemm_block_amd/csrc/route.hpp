@@ -21,6 +21,13 @@
 // A group of L lanes takes a token, V logits per lane in pieces of four, which lie side by
 // side over the lanes: lane l's v-th is logit 4 L (v / 4) + 4 l + v % 4, so that loads and
 // stores are of whole lines.
+//
+// The choice is bound by vector instructions, k rounds of E / L of them and a maximum over
+// the lanes each, not by memory: 16384 tokens, 8 of 256 experts, biased sigmoid in FP32 with
+// the load, 15.4 us (1.2 TB/s, the vector units busy 70 % of the time) and 5.8 us for the
+// sums over workgroups; 2 of 64, softmax in BF16, 8192 tokens, 5.0 + 3.1 us.  Of one token
+// it is the launch, 2.6 us.  The gradient of the large batch takes 12.5 us, 2.8 TB/s: a
+// token's loads, arithmetic and stores wait for each other, and all tokens start together.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -82,7 +89,8 @@ __device__ __forceinline__ float shifted_score(float x, float m, bool sigmoid) {
 // The branches are the wave's, not an element's: with one at each element its exponential
 // waits for the one before.
 template <bool REST, int V>
-__device__ __forceinline__ void shifted_scores(const float (&x)[V], float m, bool sigmoid, float (&s)[V], float (&rest)[REST ? V : 1]) {
+__device__ __forceinline__ void shifted_scores(const float (&x)[V], float m, bool sigmoid, float (&s)[V],
+                                               float (&rest)[REST ? V : 1]) {
   if (!sigmoid) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -150,7 +158,8 @@ __device__ __forceinline__ int value_of(int e) { return e / (4 * L) * 4 + e % 4;
 // A lane's V values of a row of E, `none` past its end.  `whole`: rows of a multiple of
 // four values, aligned to four.
 template <bool BF16, int L, int V>
-__device__ __forceinline__ void load_row(const void* x, size_t row, int l, int E, bool whole, float none, float (&v)[V]) {
+__device__ __forceinline__ void load_row(const void* x, size_t row, int l, int E, bool whole, float none,
+                                         float (&v)[V]) {
 #pragma unroll
   for (int i = 0; i < V / 4; ++i) {
     const int e = expert_of<L>(l, 4 * i);
@@ -216,11 +225,12 @@ __device__ __forceinline__ void write_loss(const RouteArgs& p, int n, double ter
 // beside whole keys takes another 36 instructions a choice.  No key is taken out: keys
 // minus the last one taken, as unsigned numbers, are in the same order, and those already
 // taken lie below all others (key - g < 2^32 - g from g on, and at least that, by wrapping
-// round, below it), so the next one is the largest again.  What the lost bits leave open is settled afterwards: the
-// choices go on past the k-th until one is certainly smaller than the one before, and
-// where two in a row were too close to tell, lane j computes the j-th one's whole key, and
-// they are ranked by those.  BF16 logits lose nothing.  Where more than a lane each are
-// too close (rows of equal logits) the choice is made again with whole keys throughout.
+// round, below it), so the next one is the largest again.  What the lost bits leave open is
+// settled afterwards: the choices go on past the k-th until one is certainly smaller than
+// the one before, and where two in a row were too close to tell, lane j computes the j-th
+// one's whole key, and they are ranked by those.  BF16 logits lose nothing.  Where more than
+// a lane each are too close (rows of equal logits) the choice is made again with whole keys
+// throughout.
 //
 // With a bias a key is of an FP32 approximation of s + bias, and the whole key of s +
 // bias in 64 bits.  A score is off by at most 2^-21 of itself (sigmoid) or 2^-18
@@ -661,8 +671,9 @@ constexpr int kRouteBwdThreads = 256;
 //   softmax, plain   u_j = scale p_j dw_j, and - p_e sum_j u_j at every expert
 //   sigmoid, plain   u_j = scale s_j (1 - s_j) dw_j
 //   loss             f_e = dloss E / (k n^2) counts_e: p_e (f_e - sum p f) [(1 - s_e)]
-// A token without choices adds nothing, whatever its logits are.  An expert that a token names twice gets both gradients, in their order.
-// The u_j reach their experts' lanes through LDS.
+// A token without choices adds nothing, whatever its logits are.  An expert that a token
+// names twice gets both gradients, in their order.  The u_j reach their experts' lanes
+// through LDS.
 template <bool BF16, int L, int V>
 __device__ __forceinline__ void route_bwd_body(const RouteBwdArgs& p) {
   constexpr int PER_BLOCK = kRouteBwdThreads / L;

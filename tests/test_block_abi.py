@@ -148,6 +148,14 @@ def test_clip_validation():
     assert clip_of([(P, 0, 0)], [(None, 0)]) == OK and clip_of([], []) == OK   # nothing to do
 
 
+@pytest.mark.parametrize("norm", [P, P + 36, P + 4 * 9999])
+def test_clip_refuses_to_write_over_its_norm(norm):
+    for n, g in ((10, 2 * P), (10, P), (10000, P)):
+        if P <= norm < P + 4 * n:
+            assert clip_of([(g, n, 0)], [(P, 0)], norm=norm) == INVALID
+            assert clip_of([(2 * P, 5, 0), (g + (g == 2 * P) * P, n, 0)], [(4 * P, 0), (P, 0)], norm=norm) == INVALID
+
+
 # ---------------------------------------------------------------- the torch side, on the CPU
 
 def test_binding_refuses_what_is_no_device_tensor():
