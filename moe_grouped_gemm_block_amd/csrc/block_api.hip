@@ -114,7 +114,16 @@ int64_t norm_bwd_most(int64_t H, bool bf16) { return H % 8 == 0 || bf16 ? dg::kN
 // (Fewer waves a workgroup would leave CUs without work to hide latency behind, more
 // workgroups would write more partial sums: 8192 rows of 512 28 us one at a time, 15 so.)
 int norm_bwd_groups(int64_t H) { return std::max(1, dg::kNormGroupThreads / norm_threads(H)); }
+// Where larger workgroups, up to `most` threads, take all rows in one turn, one on a CU:
+// fewer partial sums and none of the CUs with two turns (1009 rows of 1408, FP32 stream, 12.9
+// -> 12.2 us; 600 of 2048 12.9 -> 11.5, 512 of 4096 17.3 -> 14.8, 4000 of 512 11.7 -> 11.3).
+int norm_bwd_groups(int64_t T, int64_t H, int64_t most) {
+  const int groups = norm_bwd_groups(H);
+  const int64_t one_turn = ceil_div(T, 256);
+  return norm_wide(H, most) || one_turn * norm_threads(H) > most ? groups : std::max(groups, int(one_turn));
+}
 
+// (at most: larger workgroups are fewer)
 int64_t norm_bwd_blocks(int64_t T, int64_t H) {
   // (partial sums of 16 MB at most for wide rows)
   const int64_t most = norm_wide(H) ? std::max<int64_t>(1, (int64_t(1) << 22) / H) : 512;
@@ -374,7 +383,9 @@ int dg_residual_norm_bwd(const void* dR, const void* dN, const void* R, int r_dt
   // 4096 7.0 and 9.3)
   const bool alone = T > 0 && T <= kNormAloneTurns * norm_bwd_groups(H) && !(w_post && channel) &&
                      aligned(dw_pre, 16) && aligned(dw_post, 16) && (!channel || aligned(dgate, 16));
-  const int64_t nb = alone ? 1 : norm_bwd_blocks(T, H);
+  const int64_t most = norm_bwd_most(H, r_dtype == DG_IN_BF16 && dtype == DG_IN_BF16);
+  const int groups = norm_bwd_groups(T, H, most);
+  const int64_t nb = alone ? 1 : std::min(norm_bwd_blocks(T, H), ceil_div(T, groups));
   float* part = static_cast<float*>(workspace);
   float* part_pre = !pre ? nullptr : alone ? dw_pre : part;
   float* part_post = !post ? nullptr : alone ? (w_post ? dw_post : dgate) : part + (pre ? nb * H : 0);
@@ -386,7 +397,6 @@ int dg_residual_norm_bwd(const void* dR, const void* dN, const void* R, int r_dt
     if (dY && (dY == Y || dY == R || dY == dR || dY == dN)) return DG_ERR_INVALID_ARG;
     if ((pre || post) && !alone && bad(workspace, 16)) return DG_ERR_INVALID_ARG;
     const bool rb = r_dtype == DG_IN_BF16, yb = dtype == DG_IN_BF16, whole = H % 8 == 0;
-    const int64_t most = norm_bwd_most(H, rb && yb);
     const bool wide = norm_wide(H, most);
     const int threads = norm_threads(H, most);
     dg::NormBwdArgs a{dR, dN, pre ? R : nullptr, Y, w_post, gate, w_pre, dR_out, dY, token ? dgate : nullptr,
@@ -394,7 +404,7 @@ int dg_residual_norm_bwd(const void* dR, const void* dN, const void* R, int r_dt
                       threads / 64};
     const auto kernel = rb ? (yb ? norm_bwd_kernel<true, true>(whole, wide) : norm_bwd_kernel<true, false>(whole, wide))
                            : (yb ? norm_bwd_kernel<false, true>(whole, wide) : norm_bwd_kernel<false, false>(whole, wide));
-    const int st1 = launch(kernel, a, nb, threads * norm_bwd_groups(H), stream);
+    const int st1 = launch(kernel, a, nb, threads * groups, stream);
     if (st1 != DG_OK) return st1;
   }
   if ((!pre && !post) || alone) return DG_OK;

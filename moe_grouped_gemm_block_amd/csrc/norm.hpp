@@ -448,7 +448,7 @@ struct NormBwdArgs {
 template <bool RB, bool YB, bool WHOLE, bool WIDE>
 __device__ __forceinline__ void norm_bwd_body(const NormBwdArgs& p) {
   __shared__ double slots[kNormSlots];
-  __shared__ __attribute__((aligned(16))) float columns[WIDE ? 4 : 8 * kNormGroupThreads];
+  __shared__ __attribute__((aligned(16))) float columns[WIDE ? 4 : 8 * (WHOLE || (RB && YB) ? kNormMaxThreads : kNormWideThreads)];
   // the next row is on its way while this one is computed, where there are registers for it
   constexpr bool AHEAD = !WIDE && WHOLE && RB && YB;
   int turn = 0;

@@ -254,6 +254,16 @@ def test_norm_bwd(T, H, rt, dt):
     check_bwd(problem(T, H, rt, dt, gate="token", post=False), with_dR=False)
 
 
+@pytest.mark.parametrize("T,H", [(257, 72), (511, 4096), (513, 4088), (600, 2048), (1009, 1408), (1000, 514), (2049, 264),
+                                 (4096, 512), (4097, 511)])
+@pytest.mark.parametrize("rt,dt", [(B, B), (F, F), (F, B)])
+def test_norm_bwd_of_a_turn(T, H, rt, dt):
+    """About as many rows as the chip's workgroups hold at a time, in each one's range and past it."""
+    p = problem(T, H, rt, dt, gate="channel")
+    p["R"][T // 2] *= 1e-18                       # (with this eps the sums of one row are in 64 bits)
+    check_bwd(p, alpha=0.5, eps=1e-8)
+
+
 @pytest.mark.parametrize("gate", [None, "channel", "token"])
 @pytest.mark.parametrize("post", [True, False])
 @pytest.mark.parametrize("pre", [True, False])
