@@ -66,15 +66,15 @@ struct RouteArgs {
   float scale;
 };
 
-// e^d for d <= 0 within 2^-22 of it, 0 below -104, NaN for NaN (the product with
-// log2(e) keeps its rounding error as a second term)
+// e^d for d <= 0 within 2^-22 of it, 0 below -104, NaN for NaN: 2^h, h about d log2(e), and
+// what d is more than h log(2) as a second term
 __device__ __forceinline__ float exp_nonpos(float d) {
-  d = d < -150.f ? -150.f : d;
-  constexpr float L2E = 1.44269504088896341f, L2E_LO = 1.92596299e-8f;   // their sum is log2(e)
-  const float hi = d * L2E;
-  const float lo = __builtin_fmaf(d, L2E, -hi) + d * L2E_LO;
-  const float e = __builtin_amdgcn_exp2f(hi);
-  return __builtin_fmaf(e, lo * 0.693147180559945f, e);
+  d = __builtin_elementwise_maximum(d, -150.f);
+  constexpr float LN2 = 0.693147182464599609f, LN2_LO = -1.90465429995776e-9f;   // their sum is log(2)
+  const float h = d * 1.44269504088896341f;
+  const float more = __builtin_fmaf(h, -LN2_LO, __builtin_fmaf(h, -LN2, d));
+  const float e = __builtin_amdgcn_exp2f(h);
+  return __builtin_fmaf(e, more, e);
 }
 
 // s e^-min(m, 0) (sigmoid) or e^(x - m) (softmax) for a logit x <= m
@@ -147,6 +147,16 @@ __device__ __forceinline__ float logit(const void* x, size_t i) {
   else return static_cast<const float*>(x)[i];
 }
 
+// The key of the choice: an order key with its lowest bits replaced, moved up so that those
+// of closed experts, and no others, are at most kClosedKeys.  ZEROS: -0 as 0.
+template <uint32_t NUMBER, bool ZEROS>
+__device__ __forceinline__ uint32_t packed_key(float x, uint32_t number) {
+  static_assert(NUMBER <= kClosedKeys, "numbers of closed experts");
+  const uint32_t b = __float_as_uint(ZEROS ? x + 0.f : x);
+  const uint32_t key = b ^ (uint32_t(int32_t(b) >> 31) | 0x80000000u);
+  return ((x != x ? 0xFFFFFFFFu : key - (0x7FFFFFu - kClosedKeys)) & ~NUMBER) | number;
+}
+
 // Logit of lane l's v-th value, and back.
 template <int L>
 __device__ __forceinline__ int expert_of(int l, int v) { return 4 * L * (v / 4) + 4 * l + v % 4; }
@@ -164,7 +174,10 @@ __device__ __forceinline__ void load_row(const void* x, size_t row, int l, int E
   for (int i = 0; i < V / 4; ++i) {
     const int e = expert_of<L>(l, 4 * i);
     float* o = v + 4 * i;
-    if (whole && e < E) {
+    if (whole) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) o[c] = none;
+      if (e >= E) continue;
       if constexpr (BF16) {
         const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(x) + row + e);
         o[0] = __uint_as_float(w.x << 16);
@@ -180,7 +193,10 @@ __device__ __forceinline__ void load_row(const void* x, size_t row, int l, int E
       }
     } else {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) o[c] = e + c < E ? logit<BF16>(x, row + e + c) : none;
+      for (int c = 0; c < 4; ++c) {
+        const float w = logit<BF16>(x, row + min(e + c, E - 1));
+        o[c] = e + c < E ? w : none;
+      }
     }
   }
 }
@@ -268,9 +284,12 @@ __device__ __forceinline__ void route_body(const RouteArgs& p) {
     const long long t = t0 + wave * PER_WAVE + lane / L;
     const bool there = t < p.T && (p.mask == nullptr || p.mask[t] != 0);
     const size_t row = size_t(t) * p.E;
+    // (not known to be the same every turn: comparisons with it are cheaper than kept)
+    int E = p.E;
+    asm volatile("" : "+s"(E));
     float x[V];
     if (there) {
-      load_row<BF16, L, V>(p.x, row, l, p.E, whole, -inf, x);
+      load_row<BF16, L, V>(p.x, row, l, E, whole, -inf, x);
     } else {
 #pragma unroll
       for (int v = 0; v < V; ++v) x[v] = -inf;
@@ -282,72 +301,68 @@ __device__ __forceinline__ void route_body(const RouteArgs& p) {
     m = group_reduce<L>(m, [](float a, float b) { return __builtin_elementwise_maximum(a, b); });
     const bool open = m != -inf;
     if (!open) m = 0.f;
-    uint32_t key[V];
-    if constexpr (!BIASED) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) key[v] = order_key(x[v]);
-    }
 
     // scores of all experts (over e^min(m, 0) or e^m), where something needs them; they
     // are not kept in registers during the choice
-    bool routed = open;
-    float z = 1.f;
+    float s[V], none[1];
+    float z = 1.f, r = 1.f;
     [[maybe_unused]] float f = 1.f;                 // what makes them scores
-    [[maybe_unused]] auto biased_keys = [&](const float (&s)[V]) {
-      float bias[V];
-      load_row<false, L, V>(p.bias, 0, l, p.E, whole && p.bias_aligned, 0.f, bias);
-#pragma unroll
-      for (int v = 0; v < V; ++v) key[v] = x[v] == -inf ? 0u : order_key(__builtin_fmaf(s[v], f, bias[v]));
-    };
     if (BIASED || balance || (!p.renorm && !sigmoid)) {
-      float s[V], none[1];
       shifted_scores<false>(x, m, sigmoid, s, none);
       z = 0.f;
 #pragma unroll
       for (int v = 0; v < V; ++v) z += s[v];
       z = group_sum<L>(z);
       if (!open) z = 1.f;
-      const float r = 1.f / z;
-      if constexpr (BIASED) {
-        f = sigmoid ? exp_nonpos(fminf(m, 0.f)) : r;
-        biased_keys(s);
-        uint32_t some = 0;                          // a bias of -inf may have closed the open ones
+      r = 1.f / z;
+      if constexpr (BIASED) f = sigmoid ? exp_nonpos(fminf(m, 0.f)) : r;
+    }
+    uint32_t key[V];
+    [[maybe_unused]] auto biased = [&](const float (&s)[V], float (&sum)[V]) {
+      load_row<false, L, V>(p.bias, 0, l, E, whole && p.bias_aligned, 0.f, sum);
 #pragma unroll
-        for (int v = 0; v < V; ++v) some |= key[v];
-        routed = group_max<L>(some) != 0;
-      }
-      if (balance) {
+      for (int v = 0; v < V; ++v) sum[v] = x[v] == -inf ? -inf : __builtin_fmaf(s[v], f, sum[v]);
+    };
+    {
+      float sum[V];
+      if constexpr (BIASED) biased(s, sum);
 #pragma unroll
-        for (int i = 0; i < V / 4; ++i) {
-          float4* at = reinterpret_cast<float4*>(part[wave * PER_WAVE + lane / L] + expert_of<L>(l, 4 * i));
-          float4 sum = *at;
-          sum.x += routed ? s[4 * i] * r : 0.f;
-          sum.y += routed ? s[4 * i + 1] * r : 0.f;
-          sum.z += routed ? s[4 * i + 2] * r : 0.f;
-          sum.w += routed ? s[4 * i + 3] * r : 0.f;
-          *at = sum;
-        }
+      for (int v = 0; v < V; ++v) {
+        const uint32_t number = NUMBER - uint32_t(expert_of<L>(l, v));
+        // (-0 and 0 as sums with a bias are too close to tell anyway)
+        if constexpr (BIASED) key[v] = packed_key<NUMBER, false>(sum[v], number);
+        else key[v] = packed_key<NUMBER, true>(x[v], number);
       }
     }
 
     // lane j of the group takes choice j
     const float most = sigmoid ? 1.f : f;
-    // (moved up so that closed experts' keys, and no others, stay within kClosedKeys)
-    static_assert(NUMBER <= kClosedKeys, "numbers of closed experts");
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      key[v] = ((key[v] + kClosedKeys) & ~NUMBER) | (NUMBER - uint32_t(expert_of<L>(l, v)));
     uint32_t mine = 0, last = 0;
-    bool left = true;                               // experts to choose from
+    // (behind the open experts come closed ones, of which there are enough: more keys than
+    // choices in all)
     auto choose = [&] {
       uint32_t best = 0;
 #pragma unroll
       for (int v = 0; v < V; ++v) best = max(best, key[v] - last);
       last += group_max<L>(best);
-      left = left && last > kClosedKeys;
-      if (!left) last = 0;
     };
-    for (int j = 0; j < p.k; ++j) {
+    choose();
+    if (l == 0) mine = last;
+    const bool routed = last > kClosedKeys;         // a bias of -inf may have closed the open ones
+    if (balance) {
+      const float by = routed ? r : 0.f;
+#pragma unroll
+      for (int i = 0; i < V / 4; ++i) {
+        float4* at = reinterpret_cast<float4*>(part[wave * PER_WAVE + lane / L] + expert_of<L>(l, 4 * i));
+        float4 sum = *at;
+        sum.x = __builtin_fmaf(s[4 * i], by, sum.x);
+        sum.y = __builtin_fmaf(s[4 * i + 1], by, sum.y);
+        sum.z = __builtin_fmaf(s[4 * i + 2], by, sum.z);
+        sum.w = __builtin_fmaf(s[4 * i + 3], by, sum.w);
+        *at = sum;
+      }
+    }
+    for (int j = 1; j < p.k; ++j) {
       choose();
       if (l == j) mine = last;
     }
@@ -363,7 +378,7 @@ __device__ __forceinline__ void route_body(const RouteArgs& p) {
       choose();                                     // the one behind the last
       uint32_t behind = L == 16 ? row_rotated<15>(mine) : __shfl(mine, (lane + 1) & 63, 64);
       if (l == p.k - 1) behind = last;
-      const uint64_t pairs = (__ballot(l < p.k && behind != 0 && too_close(mine, behind)) >> base) &
+      const uint64_t pairs = (__ballot(l < p.k && behind > kClosedKeys && too_close(mine, behind)) >> base) &
                              (L == 64 ? ~uint64_t(0) : uint64_t(0xFFFF));
       close = pairs != 0;
       more = (pairs >> (p.k - 1)) & 1;
@@ -372,10 +387,10 @@ __device__ __forceinline__ void route_body(const RouteArgs& p) {
         ++n;
         const uint32_t before = last;
         choose();
-        more = last != 0 && too_close(before, last);
+        more = last > kClosedKeys && too_close(before, last);
       }
     }
-    int id = mine ? int(NUMBER - (mine & NUMBER)) : -1;
+    int id = mine > kClosedKeys ? int(NUMBER - (mine & NUMBER)) : -1;
 
     if constexpr (!WHOLE_KEYS) {
       // s + bias in 64 bits
@@ -413,9 +428,11 @@ __device__ __forceinline__ void route_body(const RouteArgs& p) {
       } else if (__ballot(close)) {
         // whole keys throughout
         if constexpr (BIASED) {
-          float s[V], none[1];
+          float s[V], sum[V], none[1];
           shifted_scores<false>(x, m, sigmoid, s, none);
-          biased_keys(s);
+          biased(s, sum);
+#pragma unroll
+          for (int v = 0; v < V; ++v) key[v] = order_key(sum[v]);
           all64();
         } else {
 #pragma unroll
