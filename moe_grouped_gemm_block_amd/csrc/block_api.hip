@@ -72,8 +72,8 @@ int check_route(int64_t T, int64_t E, int top_k) {
 // Lanes and logits per lane: a row of 16 lanes holds up to 256 experts and 16 choices.
 // More than 64 experts of few tokens go over a whole wave each, which ends sooner, many
 // over a row, which takes fewer instructions a token (256 experts, 8 choices, biased
-// sigmoid with the load, row / wave: 256 tokens 17.9 / 12.9 us, 4096 18.4 / 15.4, 8192 18.7
-// / 19.7, 16384 20.3 / 28.9; gradient 4096 5.4 / 4.9, 8192 7.4 / 8.0).
+// sigmoid with the load, row / wave: 256 tokens 14.3 / 10.4 us, 4096 15.8 / 14.9, 8192 17.4
+// / 18.7, 16384 19.6 / 26.5; gradient 4096 5.1 / 4.9, 8192 7.1 / 7.9).
 int route_lanes(int64_t T, int64_t E, int top_k) {
   return E <= 256 && top_k <= 16 && (E <= 64 || T > 4096) ? 16 : 64;
 }
@@ -83,9 +83,9 @@ int route_variant(int64_t T, int64_t E, int top_k) {
 }
 
 // Workgroups.  With the load a single one takes few tokens, which saves the second launch
-// (64 experts, a row of lanes a token: 128 tokens in two turns 6.9 us, by two launches 9.3;
-// a wave a token, 256 experts: 16 tokens in one turn 6.2 us, 64 in four 16.5, by two
-// launches 9.6).
+// (64 experts, a row of lanes a token: 128 tokens in two turns 6.4 us, by two launches 9.6;
+// a wave a token, 256 experts: 16 tokens in one turn 5.9 us, 64 in four 14.9, by two
+// launches 9.5).
 int64_t route_blocks(int64_t T, int64_t E, int top_k, bool balance) {
   const int lanes = route_lanes(T, E, top_k);
   if (balance && T <= (lanes == 16 ? 128 : 16)) return 1;
