@@ -200,7 +200,15 @@ __device__ __forceinline__ bool in_range(float sum, float per, float eps) {
 __device__ __forceinline__ float rstd_of(float sum, float per, float eps) {
   return __builtin_amdgcn_rsqf(__builtin_fmaf(sum, per, eps));
 }
-__device__ __forceinline__ double rstd_of(double sum, double per, double eps) { return 1.0 / sqrt(sum * per + eps); }
+// (from the hardware's estimate, good to 2^-23, by two steps of Newton's method: codes are
+// bound by instructions, of which a square root and a division are many)
+__device__ __forceinline__ double rstd_of(double sum, double per, double eps) {
+  const double x = __builtin_fma(sum, per, eps);
+  double r = __builtin_amdgcn_rsq(x);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) r = __builtin_fma(0.5 * r, __builtin_fma(-x * r, r, 1.0), r);
+  return x == __builtin_inf() ? 0.0 : r;
+}
 
 template <typename A, typename B>
 __device__ __forceinline__ float dot8(const A& a, const B& b) {
@@ -269,7 +277,9 @@ __device__ __forceinline__ uint2 encode8(const double (&n)[8], const float (&f)[
     r = pow2f(-e);
   } else {
     const double a = amax64();
-    s = a > 0.0 ? float(a / 448.0) : 1.f;
+    double q = a * (1.0 / 448.0);                  // and what it lacks
+    q = __builtin_fma(__builtin_fma(-q, 448.0, a), 1.0 / 448.0, q);
+    s = a > 0.0 ? float(q) : 1.f;
     r = __builtin_amdgcn_rcpf(s);
   }
   const bool far = !(s >= 0x1p-100f);

@@ -186,6 +186,41 @@ def test_step_under_graph_capture(example):
             assert torch.equal(a, b), (seed, i)
 
 
+def test_two_streams_at_once():
+    """The operators that take workspaces, on two streams: each as alone."""
+    T, E, H = 6000, 256, 1408
+    made = []
+    for seed in (1, 2):
+        g = torch.Generator().manual_seed(seed)
+        made.append([torch.randn(T, E, generator=g).cuda(), (torch.randn(E, generator=g) * 0.1).cuda()] +
+                    [torch.randn(T, H, generator=g).bfloat16().cuda() for _ in range(4)] +
+                    [torch.randn(H, generator=g).cuda() for _ in range(2)] + [torch.randn(300000, generator=g).cuda()])
+
+    def run(logits, bias, dr, dn, r, y, wa, wb, grad):
+        route = dg.moe_route(logits, 8, score="sigmoid", bias=bias)
+        dlogits = dg.moe_route_bwd(route.weights, logits, route.ids, score="sigmoid", dloss=route.loss,
+                                   counts=route.counts, routed=route.routed)
+        norms = dg.residual_norm_bwd(dr, dn, r, y, w_post=wa, w_pre=wb)
+        norm = dg.grad_norm([grad, wa])
+        clipped = dg.clip_grads([grad], norm, 1.0, out=[torch.empty_like(grad)])
+        return [t for t in (*route, dlogits, *norms, norm, *clipped) if t is not None]
+
+    alone = []
+    for m in made:
+        alone.append(run(*m))
+        torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in made]
+    got = [[], []]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(run(*made[i]))
+    torch.cuda.synchronize()
+    for want, runs in zip(alone, got):
+        for one in runs:
+            assert len(one) == len(want) and all(torch.equal(p, q) for p, q in zip(one, want))
+
+
 @pytest.mark.parametrize("T", [1, 5])
 def test_decode(example, T):
     """Roundings of the products in another order move codes by a step here and there,
