@@ -256,12 +256,6 @@ struct NormArgs {
 // the 64-bit arithmetic before.)
 template <bool POW2>
 __device__ __forceinline__ uint2 encode8(const double (&n)[8], const float (&f)[8], float& s) {
-  auto amax64 = [&] {
-    double a = 0.0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) a = fmax(a, __builtin_fabs(n[i]));
-    return group_max<16>(a);
-  };
   float amax = 0.f, r;
   if constexpr (POW2) {
 #pragma unroll
@@ -269,14 +263,20 @@ __device__ __forceinline__ uint2 encode8(const double (&n)[8], const float (&f)[
     amax = group_max<16>(amax);
     int e = pow2_exponent(amax);
     if (__builtin_expect(e != pow2_exponent(amax * (1.f + 0x1p-20f)) || e != pow2_exponent(amax * (1.f - 0x1p-20f)), 0)) {
-      const double a = amax64();
+      double a = 0.0;                              // (a loop: nothing of it is done ahead)
+#pragma unroll 1
+      for (int i = 0; i < 8; ++i) a = fmax(a, __builtin_fabs(eight_at(n, i, std::make_integer_sequence<int, 8>{})));
+      a = group_max<16>(a);
       e = max(__builtin_amdgcn_frexp_exp(a) - (__builtin_amdgcn_frexp_mant(a) > 0.875 ? 8 : 9), -126);
     }
     e = amax > 0.f ? min(e, 126) : 0;
     s = pow2f(e);
     r = pow2f(-e);
   } else {
-    const double a = amax64();
+    double a = 0.0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a = fmax(a, __builtin_fabs(n[i]));
+    a = group_max<16>(a);
     double q = a * (1.0 / 448.0);                  // and what it lacks
     q = __builtin_fma(__builtin_fma(-q, 448.0, a), 1.0 / 448.0, q);
     s = a > 0.0 ? float(q) : 1.f;
@@ -417,7 +417,7 @@ __device__ __forceinline__ void norm_body(const NormArgs& p) {
       }
       F n[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) n[i] = c < p.H ? (v[i] * pre) * w_pre[i] : F(0);
+      for (int i = 0; i < 8; ++i) n[i] = (v[i] * pre) * w_pre[i];   // (0 past the row's end, or NaN: no maximum)
       float o[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) o[i] = float(n[i]);
