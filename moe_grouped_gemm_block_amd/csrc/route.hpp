@@ -552,7 +552,6 @@ constexpr int kFinishParts = 32;
 __device__ __forceinline__ void route_finish_body(const RouteArgs& p) {
   __shared__ float sums[kFinishParts][kFinishExperts + 1];
   __shared__ int32_t counts[kFinishParts][kFinishExperts + 1];
-  __shared__ bool last;
   const int col = threadIdx.x % kFinishExperts, part = threadIdx.x / kFinishExperts;
   const int e = blockIdx.x * kFinishExperts + col;
   float sum = 0.f;
@@ -581,7 +580,9 @@ __device__ __forceinline__ void route_finish_body(const RouteArgs& p) {
   sums[part][col] = sum;
   counts[part][col] = count;
   __syncthreads();
+  if (threadIdx.x >= 64) return;                   // the rest is one wave's
   if (part == 0 && e < p.E) {
+#pragma unroll
     for (int i = 1; i < kFinishParts; ++i) {
       sum += sums[i][col];
       count += counts[i][col];
@@ -589,15 +590,21 @@ __device__ __forceinline__ void route_finish_body(const RouteArgs& p) {
     p.sums[e] = sum;
     p.counts[e] = count;
     p.terms[e] = double(sum) * count;
-    __threadfence();
   }
-  __syncthreads();
-  if (threadIdx.x == 0) last = atomicAdd(p.done, 1) == int(gridDim.x) - 1;
-  __syncthreads();
-  if (!last || threadIdx.x >= 64) return;
   __threadfence();
-  double term = 0.0;
-  for (int i = threadIdx.x; i < p.E; i += 64) term += __hip_atomic_load(&p.terms[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  int ended = 0;
+  if (threadIdx.x == 0) ended = atomicAdd(p.done, 1);
+  if (__builtin_amdgcn_readfirstlane(ended) != int(gridDim.x) - 1) return;
+  __threadfence();
+  // (all loads on their way at once)
+  double terms[kRouteMaxExperts / 64], term = 0.0;
+#pragma unroll
+  for (int i = 0; i < kRouteMaxExperts / 64; ++i) {
+    const int at = threadIdx.x + 64 * i;
+    terms[i] = at < p.E ? __hip_atomic_load(&p.terms[at], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0.0;
+  }
+#pragma unroll
+  for (int i = 0; i < kRouteMaxExperts / 64; ++i) term += terms[i];
   term = group_sum<64>(term);
   n = group_sum<64>(n);
   if (threadIdx.x == 0) write_loss(p, n, term);
