@@ -24,7 +24,7 @@
 //
 // The choice is bound by vector instructions, k rounds of E / L of them and a maximum over
 // the lanes each, not by memory: 16384 tokens, 8 of 256 experts, biased sigmoid in FP32 with
-// the load, 14.7 us (1.2 TB/s, the vector units busy about 70 % of the time) and 5.9 for the
+// the load, 14.7 us (1.2 TB/s, the vector units busy about 66 % of the time) and 5.4 for the
 // sums over workgroups; 2 of 64, softmax in BF16, 8192 tokens, 4.8 + 3.1 us.  Of one token
 // it is the launch, 2.5 us.  The gradient of the large batch takes 12.5 us, 2.8 TB/s: a
 // token's loads, arithmetic and stores wait for each other, and all tokens start together.
