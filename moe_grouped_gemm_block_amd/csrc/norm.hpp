@@ -292,8 +292,11 @@ __device__ __forceinline__ uint2 encode8(const double (&n)[8], const float (&f)[
     if (__builtin_expect(w[j] != hi || far, 0)) {
       uint32_t c = 0;
 #pragma unroll 1
-      for (int i = 0; i < 4; ++i)
-        c |= e4m3_of_f64(eight_at(n, 4 * j + i, std::make_integer_sequence<int, 8>{}) / double(s)) << (8 * i);
+      for (int i = 0; i < 4; ++i) {
+        const double q = eight_at(n, 4 * j + i, std::make_integer_sequence<int, 8>{}) / double(s);
+        // (a NaN beside the value that was not decided stays NaN)
+        c |= (q != q ? hw_codes4(float(q), 0.f, 0.f, 0.f) & 0xFFu : e4m3_of_f64(q)) << (8 * i);
+      }
       w[j] = c;
     }
   }
