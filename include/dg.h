@@ -557,7 +557,8 @@ typedef enum {
  * N is that of the sum before its rounding to r_dtype.  Rows whose squares leave
  * FP32's range have their sums in 64 bits.  NaN and infinities stay in their row; a NaN
  * of N has a NaN code, and its block's scale and other codes are those of the numbers
- * beside it.
+ * beside it; a block with a value beyond FP32's largest number has a NaN scale and NaN
+ * codes.
  * Any H from 1 to 2^22 (above: DG_ERR_UNSUPPORTED); all matrices and w_post, w_pre
  * and a channel's gate are 16-byte aligned.  eps > 0; eps and alpha finite
  * (DG_ERR_INVALID_ARG).  T == 0 is a no-op.

@@ -251,7 +251,8 @@ struct NormArgs {
 // Codes of eight values n (f: the same as FP32) of a block that 16 lanes share, and its
 // scale.  The codes are those of n / s rounded once: FP32 quotients at both ends of a
 // bracket of +-2^-20 around n / s (f is within 2^-24 of n, the reciprocal within 2^-22)
-// agree about it but for one value in 2^16, which is then divided in 64 bits.  (8192 rows of
+// agree about it but for one value in 2^16, which is then divided in 64 bits.  A block whose
+// largest is infinite in FP32 has a NaN scale, by which all its codes are NaN.  (8192 rows of
 // 4096 in BF16 to codes: 66 us, 44 by memory; the 64-bit arithmetic of the row and its
 // sums bounds it.  With all quotients in 64 bits 5 us more.)
 template <bool POW2>
@@ -269,8 +270,8 @@ __device__ __forceinline__ uint2 encode8(const double (&n)[8], const float (&f)[
       a = group_max<16>(a);
       e = max(__builtin_amdgcn_frexp_exp(a) - (__builtin_amdgcn_frexp_mant(a) > 0.875 ? 8 : 9), -126);
     }
-    e = amax > 0.f ? min(e, 126) : 0;
-    s = pow2f(e);
+    e = amax > 0.f ? e : 0;
+    s = amax < __builtin_inff() ? pow2f(e) : __builtin_nanf("");
     r = pow2f(-e);
   } else {
     double a = 0.0;
@@ -279,7 +280,7 @@ __device__ __forceinline__ uint2 encode8(const double (&n)[8], const float (&f)[
     a = group_max<16>(a);
     double q = a * (1.0 / 448.0);                  // and what it lacks
     q = __builtin_fma(__builtin_fma(-q, 448.0, a), 1.0 / 448.0, q);
-    s = a > 0.0 ? float(q) : 1.f;
+    s = !(a > 0.0) ? 1.f : float(a) < __builtin_inff() ? float(q) : __builtin_nanf("");
     r = __builtin_amdgcn_rcpf(s);
   }
   const bool far = !(s >= 0x1p-100f);

@@ -1,7 +1,8 @@
 """NaN and infinities of the normalised rows as E4M3 codes.  Needs a GPU.
 
 A NaN has a NaN code, and the block's other codes and scale are those of its numbers,
-whatever they are.  Codes and scales are compared exactly."""
+whatever they are; a block with a value that FP32 does not hold has a NaN scale and NaN
+codes.  Codes and scales are compared exactly."""
 import numpy as np
 import pytest
 import torch
@@ -62,3 +63,29 @@ def test_rows_of_nan(codes):
     assert np.array_equal(q[rows], clean[0][rows]) and np.array_equal(s[rows], clean[1][rows])
     assert is_nan(q[2]).all() and (s[2] == 1).all()
     assert is_nan(q[4, 1]) and not (q[4, 2:] & 0x7F).any() and (s[4] == 1).all()     # (the others over infinity)
+
+
+@pytest.mark.parametrize("codes", ["pow2", "amax"])
+@pytest.mark.parametrize("weight", [INF, -INF, 3e38])
+def test_blocks_past_fp32(codes, weight):
+    """Weights that bring a column past FP32's largest number: its block is NaN in those rows."""
+    p = problem(300, 400, F, F, block=False)
+    p["w_pre"][200] = weight
+    p["w_pre"][7] = 1e38                                      # in range, with values up to about 4
+    p["R"][:, 7].clamp_(-2, 2)
+    x = n(p["R"])
+    unit = x * O.rstd(x, EPS)
+    past = np.abs(unit[:, 200]) * abs(weight) > float(torch.finfo(F).max)
+    assert past.any() and np.abs(unit[:, 7]).max() < 3
+    q, s = codes_of(p, codes)
+    w = n(p["w_pre"]).copy()
+    if np.isinf(weight):
+        assert past.all()
+        w[200] = 0
+    want, scales = M.quantise(unit * w, codes == "pow2")
+    block = np.arange(400) // 128 == 1
+    ok = np.ones(s.shape, bool)
+    ok[past, 1] = False
+    assert np.array_equal(s[ok], scales[ok]) and np.isnan(s[~ok]).all()
+    assert np.array_equal(q[:, ~block], want[:, ~block]) and np.array_equal(q[~past], want[~past])
+    assert is_nan(q[past][:, block]).all()
