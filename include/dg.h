@@ -510,8 +510,8 @@ typedef enum {
  *
  * counts, prob_sums, routed and loss are all null where no load is wanted (decode);
  * workspace is then not used.  Shares whose scores all underflow are those of the
- * real numbers.  A row that holds NaN, or +inf under softmax, gives NaN weights and
- * sums and ids within [0, E).  E up to 1024, top_k up to 64 and at most 2^30 slots
+ * real numbers.  A row that holds NaN, or +inf under softmax, gives NaN weights (under
+ * sigmoid where a NaN score takes part), NaN sums, and ids within [0, E).  E up to 1024, top_k up to 64 and at most 2^30 slots
  * (DG_ERR_UNSUPPORTED); top_k > E, a scale that is not finite -> DG_ERR_INVALID_ARG.
  * T == 0 is no empty work where a load is wanted.
  */

@@ -495,6 +495,8 @@ __device__ __forceinline__ void route_body(const RouteArgs& p) {
       const float s = id >= 0 ? shifted_score(xs, mc, sigmoid) : 0.f;
       const float sum = group_sum<L>(s);
       w = id >= 0 ? p.scale * (s / sum) : 0.f;
+      // (NaN among a token's scores makes all of them NaN, but a bias may choose other experts)
+      if (BIASED && !sigmoid && id >= 0 && !(m < inf)) w = __builtin_nanf("");
     } else if (id >= 0) {
       w = p.scale * (sigmoid ? shifted_score(xs, 0.f, true) : shifted_score(xs, m, false) / z);
     }

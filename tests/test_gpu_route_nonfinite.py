@@ -1,0 +1,34 @@
+"""NaN and infinite logits in the router with a bias.  Needs a GPU."""
+import numpy as np
+import pytest
+import torch
+
+from moe_grouped_gemm_block_amd import dg
+from test_gpu_route import DEV, INF, logits, n
+
+pytestmark = pytest.mark.gpu
+
+NAN = float("nan")
+# (rows of 16 lanes and waves, one and several values a lane)
+SHAPES = [(40, 12, 4), (40, 200, 8), (4100, 200, 8), (40, 600, 8)]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    dg.lib()
+
+
+@pytest.mark.parametrize("T,E,k", SHAPES)
+@pytest.mark.parametrize("value", [NAN, INF])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_rows_without_numbers_have_no_weights(T, E, k, value, renorm):
+    """Under softmax one NaN or +inf leaves a token no scores: all its weights are NaN,
+    also where the experts that are chosen have finite logits."""
+    x = logits(T, E, torch.float32, 9)
+    x[3, E - 1] = value
+    bias = torch.zeros(E, device=DEV)
+    r = dg.moe_route(x.to(DEV), k, renormalise=renorm, bias=bias)
+    assert np.isnan(n(r.weights)[3]).all() and n(r.ids)[3].min() >= 0 and len(set(n(r.ids)[3].tolist())) == k
+    rows = [t for t in range(T) if t != 3]
+    assert np.isfinite(n(r.weights)[rows]).all()
