@@ -325,7 +325,14 @@ __device__ __forceinline__ void route_body(const RouteArgs& p) {
     };
     {
       float sum[V];
-      if constexpr (BIASED) biased(s, sum);
+      if constexpr (BIASED) {
+        if (__ballot(!(m < inf))) {                 // tokens with NaN scores: a bias of -inf closes those too
+          load_row<false, L, V>(p.bias, 0, l, E, whole && p.bias_aligned, 0.f, sum);
+#pragma unroll
+          for (int v = 0; v < V; ++v) x[v] = !(m < inf) && sum[v] == -inf ? -inf : x[v];
+        }
+        biased(s, sum);
+      }
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const uint32_t number = NUMBER - uint32_t(expert_of<L>(l, v));

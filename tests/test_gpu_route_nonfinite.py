@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from moe_grouped_gemm_block_amd import dg
-from test_gpu_route import DEV, INF, logits, n
+from test_gpu_route import DEV, INF, check, logits, n
 
 pytestmark = pytest.mark.gpu
 
@@ -32,3 +32,22 @@ def test_rows_without_numbers_have_no_weights(T, E, k, value, renorm):
     assert np.isnan(n(r.weights)[3]).all() and n(r.ids)[3].min() >= 0 and len(set(n(r.ids)[3].tolist())) == k
     rows = [t for t in range(T) if t != 3]
     assert np.isfinite(n(r.weights)[rows]).all()
+
+
+@pytest.mark.parametrize("T,E,k", SHAPES)
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("value", [NAN, INF])
+@pytest.mark.parametrize("kind", ["plain", "equal"])
+def test_a_bias_closes_experts_whose_logits_are_no_numbers(T, E, k, score, value, kind):
+    x = logits(T, E, torch.float32, 9, kind)
+    x[::3, E - 2] = value
+    x[5, E - 4:] = NAN
+    bias = torch.randn(E, generator=torch.Generator().manual_seed(1)) * 0.1
+    bias[E - 4:] = -INF
+    r = dg.moe_route(x.to(DEV), k, score=score, bias=bias.to(DEV), balance=False)
+    ids = n(r.ids)
+    assert ids.min() >= 0 and ids.max() < E - 4 and all(len(set(row)) == k for row in ids.tolist())
+    if score == "sigmoid":                        # the open experts' scores do not know of them
+        x[:, E - 4:] = -INF
+        want, _ = check(x, k, score, True, bias=bias, balance=False)
+        assert torch.equal(r.ids, want.ids) and torch.equal(r.weights, want.weights)
