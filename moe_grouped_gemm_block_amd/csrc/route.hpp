@@ -356,16 +356,15 @@ __device__ __forceinline__ void route_body(const RouteArgs& p) {
     choose();
     if (l == 0) mine = last;
     const bool routed = last > kClosedKeys;         // a bias of -inf may have closed the open ones
-    if (balance) {
-      const float by = routed ? r : 0.f;
+    if (balance && routed) {                        // (scores of other rows may be NaN)
 #pragma unroll
       for (int i = 0; i < V / 4; ++i) {
         float4* at = reinterpret_cast<float4*>(part[wave * PER_WAVE + lane / L] + expert_of<L>(l, 4 * i));
         float4 sum = *at;
-        sum.x = __builtin_fmaf(s[4 * i], by, sum.x);
-        sum.y = __builtin_fmaf(s[4 * i + 1], by, sum.y);
-        sum.z = __builtin_fmaf(s[4 * i + 2], by, sum.z);
-        sum.w = __builtin_fmaf(s[4 * i + 3], by, sum.w);
+        sum.x = __builtin_fmaf(s[4 * i], r, sum.x);
+        sum.y = __builtin_fmaf(s[4 * i + 1], r, sum.y);
+        sum.z = __builtin_fmaf(s[4 * i + 2], r, sum.z);
+        sum.w = __builtin_fmaf(s[4 * i + 3], r, sum.w);
         *at = sum;
       }
     }

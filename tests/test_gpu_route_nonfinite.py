@@ -51,3 +51,20 @@ def test_a_bias_closes_experts_whose_logits_are_no_numbers(T, E, k, score, value
         x[:, E - 4:] = -INF
         want, _ = check(x, k, score, True, bias=bias, balance=False)
         assert torch.equal(r.ids, want.ids) and torch.equal(r.weights, want.weights)
+
+
+@pytest.mark.parametrize("T,E,k", SHAPES)
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_rows_without_a_choice_add_nothing_to_the_load(T, E, k, score):
+    """Tokens whose experts a bias has closed, all of them, whatever their logits are."""
+    x = logits(T, E, torch.float32, 9)
+    bias = torch.zeros(E)
+    bias[E - 3:] = -INF
+    x[7, : E - 3] = -INF
+    x[9, : E - 3] = -INF
+    want, _ = check(x, k, score, True, bias=bias)
+    assert int(want.routed) == T - 2
+    x[7, E - 1], x[9, E - 2], x[9, E - 1] = NAN, INF, NAN
+    got = dg.moe_route(x.to(DEV), k, score=score, bias=bias.to(DEV))
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
