@@ -138,8 +138,16 @@ __device__ __forceinline__ void clip_norm_few_body(const ClipBatch& p) {
   clip_norm_of((threadIdx.x & 63) == 0 ? s : 0.0, p.norm_out);
 }
 
+// The factor f 2^e: f in [0.5, 1) with the power of two apart where FP32's normal numbers do
+// not hold it with room for the gradients, else f itself and e = 0.
+struct ClipFactor {
+  float f;
+  int e;
+  __device__ __forceinline__ float operator()(float g) const { return __builtin_ldexpf(g * f, e); }
+};
+
 template <bool IN, bool OUT>
-__device__ __forceinline__ void chunk_scaled(const ClipTensor& x, int64_t begin, int n, float f) {
+__device__ __forceinline__ void chunk_scaled(const ClipTensor& x, int64_t begin, int n, ClipFactor f) {
   int done = 0;
   if (x.whole) {
     // pieces of 16 bytes of the wider type, so that a wave's stores are of whole lines
@@ -158,7 +166,7 @@ __device__ __forceinline__ void chunk_scaled(const ClipTensor& x, int64_t begin,
         load_values<IN, V>(x.g, size_t(begin) + i, v);
       }
 #pragma unroll
-      for (int k = 0; k < V; ++k) v[k] *= f;
+      for (int k = 0; k < V; ++k) v[k] = f(v[k]);
       if constexpr (!IN && OUT)
         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(x.out) + begin + i) =
             uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
@@ -169,16 +177,18 @@ __device__ __forceinline__ void chunk_scaled(const ClipTensor& x, int64_t begin,
   for (int i = done + threadIdx.x; i < n; i += kClipThreads) {
     float v;
     load_values<IN, 1>(x.g, size_t(begin) + i, &v);
-    v *= f;
+    v = f(v);
     store_values<OUT, 1>(x.out, size_t(begin) + i, &v);
   }
 }
 
 // NaN as the norm makes every gradient NaN; an infinite one makes them 0 (and
 // infinite gradients NaN), as the formula does.
-__device__ __forceinline__ float clip_factor(float norm, float max_norm) {
+__device__ __forceinline__ ClipFactor clip_factor(float norm, float max_norm) {
   const double f = double(max_norm) / double(norm);
-  return f >= 1.0 ? 1.f : float(f);
+  if (f >= 1.0) return ClipFactor{1.f, 0};
+  const bool far = f < 0x1p-100;
+  return ClipFactor{float(far ? __builtin_amdgcn_frexp_mant(f) : f), far ? __builtin_amdgcn_frexp_exp(f) : 0};
 }
 
 // Chunks from the last on: what the norm read last is still in the caches (201 M BF16
@@ -186,9 +196,9 @@ __device__ __forceinline__ float clip_factor(float norm, float max_norm) {
 __device__ __forceinline__ void clip_scale_body(const ClipBatch& p) {
   const int chunk = p.chunks - 1 - int(block_index());
   if (chunk < 0) return;
-  const float f = clip_factor(*p.norm, p.max_norm);
+  const ClipFactor f = clip_factor(*p.norm, p.max_norm);
   const ClipTensor& x = p.t[clip_tensor(p, chunk)];
-  if (f == 1.f && x.g == x.out) return;         // in place, and nothing to change
+  if (f.f == 1.f && x.g == x.out) return;       // in place, and nothing to change
   const int64_t begin = int64_t(chunk - x.first) * kClipChunk;
   const int n = int(min(x.n - begin, int64_t(kClipChunk)));
   if (x.bf16) {
