@@ -491,7 +491,8 @@ typedef enum {
  * its choices and their weights, and the load of the experts:
  *
  *   logits      : [T][E] of `dtype` (dg_in_dtype); an expert with -inf is closed to
- *                 the token.  NaN ranks above every number.
+ *                 the token.  NaN ranks above every number.  Aligned to four elements
+ *                 if E is a multiple of 4, else to one (dlogits below too).
  *   bias        : float32 [E] or null.  With it the choice goes by s + bias,
  *                 compared in 64 bits, without it by x; weights know no bias.  An
  *                 expert whose bias is -inf is closed.
@@ -559,9 +560,9 @@ typedef enum {
  * of N has a NaN code, and its block's scale and other codes are those of the numbers
  * beside it; a block with a value beyond FP32's largest number has a NaN scale and NaN
  * codes.
- * Any H from 1 to 2^22 (above: DG_ERR_UNSUPPORTED); all matrices and w_post, w_pre
- * and a channel's gate are 16-byte aligned.  eps > 0; eps and alpha finite
- * (DG_ERR_INVALID_ARG).  T == 0 is a no-op.
+ * Any H from 1 to 2^22 (above: DG_ERR_UNSUPPORTED).  All matrices and w_post, w_pre
+ * and a channel's gate are 16-byte aligned if H is a multiple of 8, else as their
+ * elements are.  eps > 0; eps and alpha finite (DG_ERR_INVALID_ARG).  T == 0 is a no-op.
  */
 int dg_residual_norm(const void* R, int r_dtype, const void* Y, int dtype, const float* w_post,
                      const float* gate, int gate_kind, float alpha, const float* w_pre, float eps, void* R_out,

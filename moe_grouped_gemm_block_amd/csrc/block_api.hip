@@ -60,6 +60,8 @@ namespace {
 
 using namespace dg_host;
 
+int elem(int dtype) { return dtype == DG_IN_BF16 ? 2 : 4; }
+
 // ---- router ------------------------------------------------------------------------
 
 int check_route(int64_t T, int64_t E, int top_k) {
@@ -93,12 +95,19 @@ int64_t route_blocks(int64_t T, int64_t E, int top_k, bool balance) {
                            balance ? dg::kRouteMaxBlocks : 65536);
 }
 
+// Alignment of logits: of a vector of four where rows are of whole ones.
+int route_align(int dtype, int64_t E) { return (E % 4 == 0 ? 4 : 1) * elem(dtype); }
+
 bool valid_scores(int score, int renormalise, float scale) {
   return (score == DG_SCORE_SOFTMAX || score == DG_SCORE_SIGMOID) && (renormalise == 0 || renormalise == 1) &&
          isfinite(scale);
 }
 
 // ---- norms -------------------------------------------------------------------------
+
+// Alignment of a matrix or of weights: of 16 bytes where rows are of whole vectors, others
+// start at any element.
+int norm_align(int dtype, int64_t H) { return H % 8 == 0 ? 16 : elem(dtype); }
 
 // Threads of a row that fits `most` threads' registers, or of a wider one.
 int norm_threads(int64_t H, int64_t most = dg::kNormMaxThreads) {
@@ -141,8 +150,9 @@ int check_norm(int r_dtype, int dtype, const void* Y, const float* w_post, const
   // (what has no rows may have no address)
   if (T > 0 && Y == nullptr && (w_post || gate || gate_kind != DG_GATE_NONE || !w_pre)) return DG_ERR_INVALID_ARG;
   if ((gate == nullptr) != (gate_kind == DG_GATE_NONE) && !(T == 0 && gate_kind == DG_GATE_TOKEN)) return DG_ERR_INVALID_ARG;
-  if (!aligned(Y, 16) || !aligned(w_post, 16) || !aligned(gate, gate_kind == DG_GATE_TOKEN ? 4 : 16) ||
-      !aligned(w_pre, 16))
+  const int weights = norm_align(DG_IN_F32, H);
+  if (!aligned(Y, norm_align(dtype, H)) || !aligned(w_post, weights) ||
+      !aligned(gate, gate_kind == DG_GATE_TOKEN ? 4 : weights) || !aligned(w_pre, weights))
     return DG_ERR_INVALID_ARG;
   return DG_OK;
 }
@@ -176,8 +186,6 @@ void (*norm_bwd_kernel(bool whole, bool wide))(dg::NormBwdArgs) {
 }
 
 // ---- clipping ------------------------------------------------------------------------
-
-int elem(int dtype) { return dtype == DG_IN_BF16 ? 2 : 4; }
 
 // Sizes and types of a list of tensors; its chunks, or a negative status.
 int64_t clip_chunks(const int64_t* sizes, const int* dtypes, int count) {
@@ -288,7 +296,7 @@ int dg_moe_route(const void* logits, int dtype, const float* bias, const uint8_t
     return DG_ERR_INVALID_ARG;
   const int64_t nb = route_blocks(T, E, top_k, balance);
   if (balance && nb > 1 && bad(workspace, 8)) return DG_ERR_INVALID_ARG;
-  if (T > 0 && (bad(logits, 16) || bad(ids, 4) || bad(weights, 4))) return DG_ERR_INVALID_ARG;
+  if (T > 0 && (bad(logits, route_align(dtype, E)) || bad(ids, 4) || bad(weights, 4))) return DG_ERR_INVALID_ARG;
   if (T == 0 && !balance) return DG_OK;
   double* terms = static_cast<double*>(nb > 1 && balance ? workspace : nullptr);
   float* part = terms ? reinterpret_cast<float*>(terms + E) : nullptr;
@@ -321,7 +329,8 @@ int dg_moe_route_bwd(const float* dweights, const void* logits, int dtype, const
   if ((routed != nullptr) != (counts != nullptr) || (dloss != nullptr) != (counts != nullptr)) return DG_ERR_INVALID_ARG;
   if (!aligned(counts, 4) || !aligned(routed, 4) || !aligned(dloss, 4)) return DG_ERR_INVALID_ARG;
   if (T == 0) return DG_OK;
-  if (bad(dweights, 4) || bad(logits, 16) || bad(ids, 4) || bad(dlogits, 16)) return DG_ERR_INVALID_ARG;
+  const int align = route_align(dtype, E);
+  if (bad(dweights, 4) || bad(logits, align) || bad(ids, 4) || bad(dlogits, align)) return DG_ERR_INVALID_ARG;
   dg::RouteBwdArgs a{logits, ids, dweights, counts, routed, dloss, dlogits, int(T), int(E), top_k,
                      score == DG_SCORE_SIGMOID, renormalise, aligned(counts, 16), scale};
 #define DG_ROUTE_TABLE(T)                                                                                       \
@@ -341,7 +350,8 @@ int dg_residual_norm(const void* R, int r_dtype, const void* Y, int dtype, const
   if (scale_mode != DG_SCALE_AMAX && scale_mode != DG_SCALE_POW2) return DG_ERR_INVALID_ARG;
   if ((Q == nullptr) != (S == nullptr)) return DG_ERR_INVALID_ARG;
   if (T == 0) return DG_OK;
-  if (bad(R, 16) || !aligned(R_out, 16) || !aligned(N, 16) || !aligned(Q, 16) || !aligned(S, 4))
+  const int of_r = norm_align(r_dtype, H), of_y = norm_align(dtype, H);
+  if (bad(R, of_r) || !aligned(R_out, of_r) || !aligned(N, of_y) || !aligned(Q, 16) || !aligned(S, 4))
     return DG_ERR_INVALID_ARG;
   if ((R_out != nullptr) != (Y != nullptr) || (N != nullptr || Q != nullptr) != (w_pre != nullptr))
     return DG_ERR_INVALID_ARG;
@@ -390,9 +400,10 @@ int dg_residual_norm_bwd(const void* dR, const void* dN, const void* R, int r_dt
   float* part_pre = !pre ? nullptr : alone ? dw_pre : part;
   float* part_post = !post ? nullptr : alone ? (w_post ? dw_post : dgate) : part + (pre ? nb * H : 0);
   if (T > 0) {
-    if (bad(dR_out, 16) || !aligned(dR, 16) || (token && bad(dgate, 4))) return DG_ERR_INVALID_ARG;
-    if (pre ? bad(R, 16) || bad(dN, 16) : dN != nullptr || dR == nullptr) return DG_ERR_INVALID_ARG;
-    if ((dY != nullptr) != (Y != nullptr) || !aligned(dY, 16)) return DG_ERR_INVALID_ARG;
+    const int of_r = norm_align(r_dtype, H), of_y = norm_align(dtype, H);
+    if (bad(dR_out, of_r) || !aligned(dR, of_r) || (token && bad(dgate, 4))) return DG_ERR_INVALID_ARG;
+    if (pre ? bad(R, of_r) || bad(dN, of_y) : dN != nullptr || dR == nullptr) return DG_ERR_INVALID_ARG;
+    if ((dY != nullptr) != (Y != nullptr) || !aligned(dY, of_y)) return DG_ERR_INVALID_ARG;
     if (dR_out == dR || dR_out == R || dR_out == dN || dR_out == Y || dR_out == dY) return DG_ERR_INVALID_ARG;
     if (dY && (dY == Y || dY == R || dY == dR || dY == dN)) return DG_ERR_INVALID_ARG;
     if ((pre || post) && !alone && bad(workspace, 16)) return DG_ERR_INVALID_ARG;
