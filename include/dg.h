@@ -478,7 +478,7 @@ int dg_grouped_wgrad_fp8(const void* dY, const void* X, const float* sX, const i
  * router in front of it, the norms around it, and the clipping of its gradients.
  * The shared conventions above apply: caller-owned device memory, asynchronous on
  * `stream`, host-side argument checks before any HIP call, nothing atomic whose
- * order shows, results bitwise repeatable, no allocation, capturable into a HIP
+ * order shows, results bitwise repeatable, no device allocation, capturable into a HIP
  * graph.  Outputs must not overlap inputs or each other unless a call says so.
  */
 typedef enum {
@@ -603,8 +603,10 @@ int dg_grad_norm(const void* const* grads, const int64_t* sizes, const int* dtyp
 /*
  * Clipping: outs[i] = grads[i] min(1, max_norm / norm), with norm float32 [1] on the
  * device.  outs[i] may be grads[i] (of the same type then) and must not overlap
- * anything else in the lists, nor norm (DG_ERR_INVALID_ARG).  A norm of NaN gives NaN, an
- * infinite one zeros and, for infinite elements, NaN.  max_norm finite and positive.
+ * anything else in the lists, nor norm (DG_ERR_INVALID_ARG); the check takes 48 bytes of host
+ * memory a tensor until the call returns (DG_ERR_LAUNCH where there are none, nothing is
+ * launched then).  A norm of NaN gives NaN, an infinite one zeros and, for infinite elements,
+ * NaN.  max_norm finite and positive.
  */
 int dg_clip_grads(const void* const* grads, const int64_t* sizes, const int* dtypes, int count,
                   const float* norm, float max_norm, void* const* outs, const int* out_dtypes,

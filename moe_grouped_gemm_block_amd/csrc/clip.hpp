@@ -191,8 +191,9 @@ __device__ __forceinline__ ClipFactor clip_factor(float norm, float max_norm) {
   return ClipFactor{float(far ? __builtin_amdgcn_frexp_mant(f) : f), far ? __builtin_amdgcn_frexp_exp(f) : 0};
 }
 
-// Chunks from the last on: what the norm read last is still in the caches (201 M BF16
-// into FP32 191 us, from the first on 215).
+// Chunks from a launch's last on: what the norm read last is still in the caches (201 M BF16 in
+// 48 tensors into FP32 191 us, from the first on 215).  Lists of several launches go through
+// these in their order, each from its last chunk.
 __device__ __forceinline__ void clip_scale_body(const ClipBatch& p) {
   const int chunk = p.chunks - 1 - int(block_index());
   if (chunk < 0) return;

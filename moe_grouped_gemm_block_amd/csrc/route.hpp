@@ -22,11 +22,13 @@
 // side over the lanes: lane l's v-th is logit 4 L (v / 4) + 4 l + v % 4, so that loads and
 // stores are of whole lines.
 //
-// The choice is bound by vector instructions, k rounds of E / L of them and a maximum over
-// the lanes each, not by memory: 16384 tokens, 8 of 256 experts, biased sigmoid in FP32 with
-// the load, 14.7 us (1.2 TB/s, the vector units busy about 66 % of the time) and 5.4 for the
-// sums over workgroups; 2 of 64, softmax in BF16, 8192 tokens, 4.8 + 3.1 us.  Of one token
-// it is the launch, 2.5 us.  The gradient of the large batch takes 12.5 us, 2.8 TB/s: a
+// The forward pass is bound by vector instructions, not by memory: 16384 tokens, 8 of 256
+// experts, biased sigmoid in FP32 with the load, 14.7 us (1.2 TB/s, the vector units busy about
+// 66 % of the time) and 5.4 for the sums over workgroups; 2 of 64, softmax in BF16, 8192 tokens,
+// 4.8 + 3.1 us.  Of the 1105 that a wave of the large batch takes, counted in the assembly,
+// about 280 are the choice (nine rounds of 16 keys a lane and a maximum over 16 lanes), 220 the
+// scores, 200 the biased sums and their keys, 70 loads and the largest logit, 70 the weights, 20
+// the sums of p, the rest what a workgroup does once.  Of one token it is the launch, 2.5 us.  The gradient of the large batch takes 12.5 us, 2.8 TB/s: a
 // token's loads, arithmetic and stores wait for each other, and all tokens start together.
 #pragma once
 
@@ -66,8 +68,9 @@ struct RouteArgs {
   float scale;
 };
 
-// e^d for d <= 0 within 2^-22 of it, 0 below -104, NaN for NaN: 2^h, h about d log2(e), and
-// what d is more than h log(2) as a second term
+// e^d for d <= 0, NaN for NaN: 2^h, h about d log2(e), and what d is more than h log(2) as a
+// second term.  Within 2^-22 of it where it is a normal number of FP32 (d >= -87); below 2^-126
+// it has few bits or is 0.
 __device__ __forceinline__ float exp_nonpos(float d) {
   d = __builtin_elementwise_maximum(d, -150.f);
   constexpr float LN2 = 0.693147182464599609f, LN2_LO = -1.90465429995776e-9f;   // their sum is log(2)
