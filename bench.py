@@ -80,16 +80,19 @@ def log(*a):
     print(*a, file=sys.stderr, flush=True)
 
 
+# Sources of the operators around the products and around a block, which are not measured here
+# and which no measured one includes.
+AROUND = {"binding.cpp", "kernels_wgrad.hip", "moe.hpp", "moe_api.hip", "swiglu.hpp", "wgrad.hpp",
+          "block_api.hip", "clip.hpp", "groups.hpp", "host.hpp", "norm.hpp", "route.hpp"}
+
+
 def kernel_source_hash() -> str:
-    """Hash of the products' and the quantiser's kernel sources and of their compiler flags;
-    the operators around the products and around a block are not measured here."""
+    """Hash of the products' and the quantiser's kernel sources and of their compiler flags."""
     from moe_grouped_gemm_block_amd import build
 
     h = hashlib.sha256()
-    around = {"binding.cpp", "kernels_wgrad.hip", "moe.hpp", "moe_api.hip", "swiglu.hpp", "wgrad.hpp",
-              "block_api.hip", "clip.hpp", "groups.hpp", "host.hpp", "norm.hpp", "route.hpp"}
     files = sorted(f for f in glob.glob(os.path.join(ROOT, "moe_grouped_gemm_block_amd", "csrc", "*"))
-                   if os.path.basename(f) not in around)
+                   if os.path.basename(f) not in AROUND)
     for f in files:
         h.update(os.path.basename(f).encode())
         h.update(open(f, "rb").read())
