@@ -24,8 +24,8 @@
 //
 // The forward pass is bound by vector instructions, not by memory: 16384 tokens, 8 of 256
 // experts, biased sigmoid in FP32 with the load, 14.7 us (1.2 TB/s, the vector units busy about
-// 66 % of the time) and 5.4 for the sums over workgroups; 2 of 64, softmax in BF16, 8192 tokens,
-// 4.8 + 3.1 us.  Of the 1105 that a wave of the large batch takes, counted in the assembly,
+// 67 % of the time) and 5.4 for the sums over workgroups; 2 of 64, softmax in BF16, 8192 tokens,
+// 4.8 + 3.1 us.  Of the 1106 that a wave of the large batch takes, counted in the assembly,
 // about 280 are the choice (nine rounds of 16 keys a lane and a maximum over 16 lanes), 220 the
 // scores, 200 the biased sums and their keys, 70 loads and the largest logit, 70 the weights, 20
 // the sums of p, the rest what a workgroup does once.  Of one token it is the launch, 2.5 us.  The gradient of the large batch takes 12.5 us, 2.8 TB/s: a
