@@ -367,7 +367,8 @@ int dg_residual_norm(const void* R, int r_dtype, const void* Y, int dtype, const
   const auto kernel = rb ? (yb ? norm_kernel<true, true>(codes, whole, wide) : norm_kernel<true, false>(codes, whole, wide))
                          : (yb ? norm_kernel<false, true>(codes, whole, wide) : norm_kernel<false, false>(codes, whole, wide));
   // as many workgroups as are there at a time by their registers, three of 8 waves a CU, for
-  // codes two (8192 rows of 4096: 2 a CU 48.5, 3 47.5, 4 51 us; codes 2 66, 3 70)
+  // codes two (8192 rows of 4096: 2 a CU 48.5, 3 47.5, 4 51 us; codes 2 66, 3 70).  One of 13 to
+  // 16 waves for 6145 to 8192 columns keeps up too (4096 rows of 8192 46 us, 5.8 TB/s)
   return launch(kernel, a, std::min<int64_t>(T, 256 * std::max(1, (Q ? 16 : 24) / (threads / 64))), threads, stream);
 }
 
