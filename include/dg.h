@@ -512,9 +512,10 @@ typedef enum {
  * counts, prob_sums, routed and loss are all null where no load is wanted (decode);
  * workspace is then not used.  Shares whose scores all underflow are those of the
  * real numbers.  A row that holds NaN, or +inf under softmax, gives NaN weights (under
- * sigmoid where a NaN score takes part), NaN sums, and ids within [0, E).  E up to 1024, top_k up to 64 and at most 2^30 slots
- * (DG_ERR_UNSUPPORTED); top_k > E, a scale that is not finite -> DG_ERR_INVALID_ARG.
- * T == 0 is no empty work where a load is wanted.
+ * sigmoid where a NaN score takes part), NaN sums, and ids within [0, E).  E up to
+ * 1024, top_k up to 64 and at most 2^30 slots (DG_ERR_UNSUPPORTED); top_k > E, a scale
+ * that is not finite -> DG_ERR_INVALID_ARG.  T == 0 is no empty work where a load is
+ * wanted.
  */
 int64_t dg_moe_route_workspace(int64_t T, int64_t E, int top_k);
 int dg_moe_route(const void* logits, int dtype, const float* bias, const uint8_t* mask, int64_t T, int64_t E,
@@ -580,6 +581,7 @@ int dg_residual_norm(const void* R, int r_dtype, const void* Y, int dtype, const
  *   workspace : dg_residual_norm_bwd_workspace(T, H, sums) bytes, 16-byte aligned,
  *             where sums counts w_pre, and w_post or a channel's gate (0 to 2)
  *
+ * Matrices and weights are aligned as there, dw_post, dgate and dw_pre to elements.
  * T == 0 is no empty work: the weights' gradients are written (zeros).
  */
 int64_t dg_residual_norm_bwd_workspace(int64_t T, int64_t H, int sums);
